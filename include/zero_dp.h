@@ -60,6 +60,28 @@ extern "C" {
 /* ---- dtypes (values are part of the ABI) -------------------------------- */
 #define ZERO_DT_F16 1  /* IEEE binary16 */
 #define ZERO_DT_BF16 2 /* bfloat16 */
+#define ZERO_DT_F32 3  /* fp32 (the zero_mx_* calls only) */
+
+/* ---- microscaled 4-bit format (MXFP4) ------------------------------------
+ * Blocks of ZERO_MX_BLOCK consecutive values share one scale byte (E8M0:
+ * 2^(byte - 127); 255 marks a NaN block), and each value is a 4-bit E2M1 code:
+ * a sign bit (8) and a magnitude code 0..7 for 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ * Two codes a byte, the even element in the low nibble, so a block is 16 bytes
+ * of codes and one scale byte: 17 bytes for 32 values. Codes and scales are
+ * separate arrays: block b at codes + 16 * b and scales + b.
+ *   Flat vector: value j lies in block j / 32; a shard starts at a multiple of
+ *     32 (zero_partition with align_elems a multiple of 32 * n_d gives such
+ *     segments). A shard that ends inside a block owns the whole block.
+ *   Matrix rows x cols: every row is ceil(cols / 32) blocks, its last block
+ *     filled up with zero codes; `ld` blocks lie from one row to the next (in
+ *     codes and in scales alike). A tensor of a flat vector whose rows are a
+ *     multiple of 32 values is such a matrix, in place.
+ * Quantising a block: amax = the largest magnitude, byte =
+ *   max(floor(log2(amax)) - 2, -127) + 127 (0 for a block of zeros), codes =
+ *   value / 2^(byte - 127) rounded to nearest even, saturating at +-6, the sign
+ *   kept. A block that holds inf or NaN becomes a NaN block (byte 255, codes 0).
+ * Alignment: codes 16 bytes, scales any, values their own size. */
+#define ZERO_MX_BLOCK 32
 
 /* One rank's segment of a flat vector: elements [offset, offset + size). */
 typedef struct {
@@ -343,6 +365,73 @@ int zero_adam_step_static(const zero_group* groups, int32_t n_groups, const zero
  * parameters from the master. Errors: INVALID_ARG, ALIGNMENT. */
 int zero_cast_writeback(const float* master, int64_t n, void* flat_param, int64_t offset,
                         int32_t param_dt, void* stream);
+
+/* ---- microscaled 4-bit calls -----------------------------------------------
+ * The step's outputs and inputs in 4 bits: what the ranks exchange around the
+ * step (the written segment and the gradient copies) at 17/32 byte per value
+ * instead of 2, and the products of a layer on tensors in that format. Not an
+ * operation of the pages, which keep both in 16 bits. None of these calls but
+ * the average reads or writes a zero_step_state. Outputs must not overlap
+ * inputs. */
+
+/* zero_cast_writeback into a 4-bit flat vector: quantise master[0..n) into
+ * elements [offset, offset + n) of the vector at codes / scales. offset must be
+ * a multiple of 32. If n is not, the rest of the last block gets zero codes;
+ * nothing past that block is touched.
+ * Errors: INVALID_ARG, ALIGNMENT. */
+int zero_mx_cast_writeback(const float* master, int64_t n, void* codes, void* scales, int64_t offset, void* stream);
+
+/* Quantise a matrix of `rows` rows of `cols` values of src_dt (F32, F16 or
+ * BF16), src_ld >= cols values from row to row, in one pass into either or both
+ * of
+ *   codes, scales:     the matrix, blocks along its rows
+ *                      (rows x ceil(cols / 32) blocks, ld from row to row);
+ *   codes_t, scales_t: its transpose, blocks along the columns
+ *                      (cols x ceil(rows / 32) blocks, ld_t from row to row).
+ * A NULL codes (codes_t) leaves that one out; its scales must be NULL too. The
+ * product needs its operands' blocks along the contraction, so a layer's
+ * forward takes the first and its gradients the second. Blocks past a row's
+ * last one (where ld is larger) are left as they are.
+ * Errors: INVALID_ARG, ALIGNMENT. */
+int zero_mx_quantize(const void* src, int32_t src_dt, int64_t rows, int64_t cols, int64_t src_ld, void* codes,
+                     void* scales, int64_t ld, void* codes_t, void* scales_t, int64_t ld_t, void* stream);
+
+/* The values of a 4-bit matrix: out[i * out_ld + j] = code * scale for j < cols,
+ * rounded once to out_dt (exact in BF16 and, short of overflow to inf at the
+ * largest scales, in F32; F16 rounds to nearest even). A NaN block gives the
+ * canonical quiet NaN. A flat slice is one row (codes and scales at its first
+ * block).
+ * Errors: INVALID_ARG, ALIGNMENT. */
+int zero_mx_dequantize(const void* codes, const void* scales, int64_t rows, int64_t cols, int64_t ld, void* out,
+                       int32_t out_dt, int64_t out_ld, void* stream);
+
+/* zero_reduce_grad_segment over copies in 4 bits: codes[r] / scales[r] (host
+ * arrays of n_d device pointers) hold copy r of this rank's segment as a flat
+ * vector of n values. Sums, average, norm partials and overflow flag are those
+ * of zero_reduce_grad_segment on the values the codes stand for; a NaN block in
+ * a copy (what quantising an inf or NaN gives) sets the flag. avg_out feeds
+ * zero_grad_norm_overflow() and zero_adam_step() as usual. More than 64 copies
+ * must be equally spaced, codes and scales each.
+ * Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, UNSUPPORTED (n_d too large). */
+int zero_mx_reduce_grad_segment(const void* const* codes, const void* const* scales, int32_t n_d, int64_t n,
+                                float* avg_out, void* workspace, size_t workspace_bytes, int32_t group,
+                                const zero_step_state* state, void* stream);
+
+/* Product of two 4-bit matrices along their rows: for i < m, j < n
+ *   out[i * ldo + j] = sum over k of A[i][k] * B[j][k],
+ * A m x (32 * k_blocks) with lda blocks from row to row, B n x (32 * k_blocks)
+ * with ldb. Products are exact, sums are fp32 (in an order that depends on the
+ * sizes only, so results repeat bit for bit), and out is rounded once to out_dt
+ * (F32, or F16 / BF16 to nearest even). A NaN block makes every output of its
+ * row NaN. k_blocks = 0 gives zeros. Of a linear layer with weight W (out x in)
+ * all three products have this form: y = x W^T from x and W along their rows,
+ * dx = dy W from dy and the transposed copy of W, dW = dy^T x from the
+ * transposed copies of dy and x.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (more than 2^31 - 1 rows in A or
+ * B, or output tiles past a launch's limit). */
+int zero_mx_product(const void* a_codes, const void* a_scales, int64_t lda, const void* b_codes, const void* b_scales,
+                    int64_t ldb, int64_t m, int64_t n, int64_t k_blocks, void* out, int32_t out_dt, int64_t ldo,
+                    void* stream);
 
 /* ---- testing --------------------------------------------------------------
  * Not an operation of the pages. Caps the blocks of every streaming launch

@@ -23,13 +23,17 @@ MAX_GROUPS = 8
 MAX_REPLICAS = 4096
 DT_F16 = 1
 DT_BF16 = 2
+DT_F32 = 3
+MX_BLOCK = 32
 HBM_REGION_BYTES = 96 << 30
 ARENA_ALIGN = 2 << 20
 
 EXPORTS = ("zero_partition", "zero_partition_tensors", "zero_workspace_bytes",
            "zero_last_error", "zero_state_init", "zero_reduce_grad_segment",
            "zero_grad_norm_overflow", "zero_adam_step", "zero_cast_writeback", "zero_plan_arena",
-           "zero_set_grid_limit", "zero_adam_step_static", "zero_copy_probe")
+           "zero_set_grid_limit", "zero_adam_step_static", "zero_copy_probe",
+           "zero_mx_cast_writeback", "zero_mx_quantize", "zero_mx_dequantize",
+           "zero_mx_reduce_grad_segment", "zero_mx_product")
 
 
 class ZeroError(RuntimeError):
@@ -125,6 +129,12 @@ def load():
         L.zero_set_grid_limit.argtypes = [i32]
         L.zero_adam_step_static.argtypes = [ctypes.POINTER(_Group), i32, ctypes.POINTER(Policy), vp, vp]
         L.zero_copy_probe.argtypes = [vp, vp, vp, vp, i64, vp]
+        L.zero_mx_cast_writeback.argtypes = [vp, i64, vp, vp, i64, vp]
+        L.zero_mx_quantize.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, vp, vp, i64, vp]
+        L.zero_mx_dequantize.argtypes = [vp, vp, i64, i64, i64, vp, i32, i64, vp]
+        L.zero_mx_reduce_grad_segment.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(vp), i32, i64, vp, vp, sz, i32,
+                                                  vp, vp]
+        L.zero_mx_product.argtypes = [vp, vp, i64, vp, vp, i64, i64, i64, i64, vp, i32, i64, vp]
         for name in EXPORTS:
             fn = getattr(L, name)
             if name not in ("zero_workspace_bytes", "zero_last_error"):
@@ -514,3 +524,191 @@ def cast_writeback(master, flat_param, offset, stream=None):
         raise ValueError("offset + n exceeds the flat parameter vector")
     _check(load().zero_cast_writeback(_ptr(master), n, _ptr(flat_param), offset, _dt(flat_param),
                                       _stream(stream)))
+
+
+# --------------------------------------------------------------------------
+# microscaled 4-bit format: uint8 codes (16 bytes per 32 values) and uint8
+# scales (1 per 32 values); see include/zero_dp.h
+# --------------------------------------------------------------------------
+
+def mx_empty(rows, cols, device="cuda"):
+    """(codes, scales) of a rows x cols matrix in 4 bits, uninitialised."""
+    torch = _torch()
+    kb = -(-cols // MX_BLOCK)
+    return (torch.empty(rows, 16 * kb, dtype=torch.uint8, device=device),
+            torch.empty(rows, kb, dtype=torch.uint8, device=device))
+
+
+def mx_view(codes, scales, offset, rows, cols):
+    """The rows x cols tensor at element `offset` of a flat 4-bit vector, as the
+    (codes, scales) matrix the other calls take. Offset and cols must be
+    multiples of 32 (its rows are then whole blocks)."""
+    if offset < 0 or offset % MX_BLOCK or cols % MX_BLOCK:
+        raise ValueError(f"offset {offset} and cols {cols} must be multiples of {MX_BLOCK}")
+    b, n = offset // MX_BLOCK, rows * cols // MX_BLOCK
+    if codes.dim() != 1 or scales.dim() != 1 or scales.numel() < b + n or codes.numel() < 16 * (b + n):
+        raise ValueError("the tensor does not lie inside the flat vector")
+    return (codes[16 * b:16 * (b + n)].view(rows, cols // 2), scales[b:b + n].view(rows, cols // MX_BLOCK))
+
+
+def _mx_types():
+    torch = _torch()
+    return (torch.float32, torch.float16, torch.bfloat16)
+
+
+def _mx_dt(t):
+    return DT_F32 if t.dtype == _torch().float32 else _dt(t)
+
+
+def _on(device):
+    """The device context and the stream argument of a call on `device`'s
+    tensors (its current stream unless the caller names one)."""
+    return _torch().cuda.device(device)
+
+
+def _device_of(t, name):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    return t.device
+
+
+def _need_rows(t, name, dtypes, device):
+    """A 2-D tensor of one of `dtypes` on `device` with dense rows; the elements from row to row."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: a torch tensor is expected, got {type(t).__name__}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if t.device != device:
+        raise ValueError(f"{name}: tensor on {t.device}, expected {device}")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: {t.dim()} dimensions, expected 2")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: its rows are not dense")
+    if rows <= 1:
+        return max(1, cols)
+    if t.stride(0) < cols:
+        raise ValueError(f"{name}: rows overlap")
+    return t.stride(0)
+
+
+def _need_mx(codes, scales, name, device, rows=None, values=None):
+    """A 4-bit matrix (2-D codes and scales); its blocks from row to row."""
+    u8 = (_torch().uint8,)
+    ld_c = _need_rows(codes, f"{name} codes", u8, device)
+    ld_s = _need_rows(scales, f"{name} scales", u8, device)
+    r, kb = scales.shape
+    if tuple(codes.shape) != (r, 16 * kb):
+        raise ValueError(f"{name}: codes {tuple(codes.shape)} do not match scales {tuple(scales.shape)}: "
+                         f"expected {(r, 16 * kb)}")
+    if rows is not None and r != rows:
+        raise ValueError(f"{name}: {r} rows, expected {rows}")
+    if values is not None and kb != -(-values // MX_BLOCK):
+        raise ValueError(f"{name}: {kb} blocks a row, expected {-(-values // MX_BLOCK)}")
+    if r > 1 and kb > 0 and ld_c != 16 * ld_s:
+        raise ValueError(f"{name}: rows of codes lie {ld_c} bytes apart and rows of scales {ld_s}: expected 16 to 1")
+    return max(ld_s, kb)
+
+
+def _need_flat(codes, scales, name, device, offset, n):
+    """A flat 4-bit vector that holds elements [offset, offset + n)."""
+    u8 = (_torch().uint8,)
+    _need(codes, f"{name} codes", u8, device)
+    _need(scales, f"{name} scales", u8, device)
+    if offset < 0 or offset % MX_BLOCK:
+        raise ValueError(f"{name}: offset {offset} is not a multiple of {MX_BLOCK}")
+    end = offset // MX_BLOCK + -(-n // MX_BLOCK)
+    if scales.numel() < end or codes.numel() < 16 * end:
+        raise ValueError(f"{name}: offset + n exceeds the flat vector")
+    return end
+
+
+def mx_cast_writeback(master, codes, scales, offset=0, stream=None):
+    """cast_writeback into a flat 4-bit vector, at element `offset` (a multiple
+    of 32). A shard that ends inside a block must end the vector: the block's
+    other values would belong to the next rank."""
+    dev = _device_of(master, "master")
+    _need(master, "master", _f32(), dev)
+    n = master.numel()
+    end = _need_flat(codes, scales, "flat vector", dev, offset, n)
+    if n % MX_BLOCK and end != scales.numel():
+        raise ValueError(f"a shard of {n} values ends inside a block that is not the vector's last one")
+    with _on(dev):
+        _check(load().zero_mx_cast_writeback(_ptr(master), n, _ptr(codes), _ptr(scales), offset, _stream(stream)))
+
+
+def mx_quantize(src, codes=None, scales=None, codes_t=None, scales_t=None, stream=None):
+    """Quantise a 2-D fp32/fp16/bf16 tensor along its rows into (codes, scales)
+    and / or along its columns into (codes_t, scales_t), the transposed matrix;
+    allocate them with mx_empty(rows, cols) and mx_empty(cols, rows)."""
+    dev = _device_of(src, "src")
+    src_ld = _need_rows(src, "src", _mx_types(), dev)
+    rows, cols = src.shape
+    if (codes is None) != (scales is None) or (codes_t is None) != (scales_t is None):
+        raise ValueError("codes and scales must be given together")
+    if codes is None and codes_t is None:
+        raise ValueError("no output")
+    ld = _need_mx(codes, scales, "output", dev, rows, cols) if codes is not None else 0
+    ld_t = _need_mx(codes_t, scales_t, "transposed output", dev, cols, rows) if codes_t is not None else 0
+    with _on(dev):
+        _check(load().zero_mx_quantize(_ptr(src), _mx_dt(src), rows, cols, src_ld, _ptr(codes), _ptr(scales), ld,
+                                       _ptr(codes_t), _ptr(scales_t), ld_t, _stream(stream)))
+
+
+def mx_dequantize(codes, scales, out, offset=0, stream=None):
+    """The values of a 4-bit matrix (2-D codes, scales and out), or of elements
+    [offset, offset + out.numel()) of a flat 4-bit vector (1-D), in out's dtype
+    (fp32, fp16 or bf16)."""
+    dev = _device_of(out, "out")
+    if out.dim() == 1:
+        _need(out, "out", _mx_types(), dev)
+        rows, cols = 1, out.numel()
+        _need_flat(codes, scales, "flat vector", dev, offset, cols)
+        b = offset // MX_BLOCK
+        cp, sp = ctypes.c_void_p(codes.data_ptr() + 16 * b), ctypes.c_void_p(scales.data_ptr() + b)
+        ld, out_ld = -(-cols // MX_BLOCK), cols
+    else:
+        if offset:
+            raise ValueError("offset is for flat vectors")
+        out_ld = _need_rows(out, "out", _mx_types(), dev)
+        rows, cols = out.shape
+        ld = _need_mx(codes, scales, "input", dev, rows, cols)
+        cp, sp = _ptr(codes), _ptr(scales)
+    with _on(dev):
+        _check(load().zero_mx_dequantize(cp, sp, rows, cols, ld, _ptr(out), _mx_dt(out), out_ld, _stream(stream)))
+
+
+def mx_reduce_grad_segment(codes, scales, avg_out, workspace, group, state, stream=None):
+    """reduce_grad_segment over copies in 4 bits: codes and scales are lists of
+    N_d flat vectors (1-D uint8), each holding the segment from element 0."""
+    dev = _state_device(state, workspace)
+    _need(avg_out, "avg_out", _f32(), dev)
+    n = avg_out.numel()
+    if not codes or len(codes) != len(scales):
+        raise ValueError(f"{len(codes)} copies of codes and {len(scales)} of scales")
+    for r, (c, s) in enumerate(zip(codes, scales)):
+        _need_flat(c, s, f"copy {r}", dev, 0, n)
+    with _on(dev):
+        _check(load().zero_mx_reduce_grad_segment(_ptr_array(codes), _ptr_array(scales), len(codes), n, _ptr(avg_out),
+                                                  _ptr(workspace), _nbytes(workspace), group, _ptr(state),
+                                                  _stream(stream)))
+
+
+def mx_product(a_codes, a_scales, b_codes, b_scales, out, stream=None):
+    """out[i, j] = sum_k A[i, k] * B[j, k] of two 4-bit matrices (2-D codes and
+    scales, blocks along k), into a 2-D fp32/fp16/bf16 tensor. For a linear
+    layer: y = x W^T takes x and W, dx = dy W takes dy and W's transposed copy,
+    dW = dy^T x takes the transposed copies of dy and x (mx_quantize)."""
+    dev = _device_of(out, "out")
+    ldo = _need_rows(out, "out", _mx_types(), dev)
+    m, n = out.shape
+    lda = _need_mx(a_codes, a_scales, "A", dev, m)
+    ldb = _need_mx(b_codes, b_scales, "B", dev, n)
+    kb = a_scales.shape[1]
+    if b_scales.shape[1] != kb:
+        raise ValueError(f"A has {kb} blocks a row, B {b_scales.shape[1]}")
+    with _on(dev):
+        _check(load().zero_mx_product(_ptr(a_codes), _ptr(a_scales), lda, _ptr(b_codes), _ptr(b_scales), ldb, m, n, kb,
+                                      _ptr(out), _mx_dt(out), max(ldo, n), _stream(stream)))

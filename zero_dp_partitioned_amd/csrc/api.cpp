@@ -10,7 +10,7 @@
 #include <vector>
 #include <unordered_map>
 
-#include "zero_dp_internal.h"
+#include "api_common.h"
 
 using namespace zdp;
 
@@ -22,8 +22,10 @@ hipError_t launch_copy_probe(const void* src0, const void* src1, void* dst0, voi
 }  // namespace zdp
 
 namespace {
-
 thread_local char g_err[512] = "";
+}  // namespace
+
+namespace zdp {
 
 int fail(int code, const char* fmt, ...) {
   va_list ap;
@@ -37,9 +39,58 @@ int hip_fail(hipError_t e, const char* what) {
   return fail(ZERO_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-bool valid_dt(int32_t dt) { return dt == ZERO_DT_F16 || dt == ZERO_DT_BF16; }
+// The current device must be gfx950. *info (optional) receives its DeviceInfo.
+int check_device(DeviceInfo* info) {
+  static std::mutex mu;
+  static std::unordered_map<int, DeviceInfo> known;
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+  std::lock_guard<std::mutex> lk(mu);
+  auto it = known.find(dev);
+  if (it == known.end()) {
+    hipDeviceProp_t prop;
+    e = hipGetDeviceProperties(&prop, dev);
+    if (e != hipSuccess) return hip_fail(e, "hipGetDeviceProperties");
+    int lds = 0;
+    e = hipDeviceGetAttribute(&lds, hipDeviceAttributeMaxSharedMemoryPerMultiprocessor, dev);
+    if (e != hipSuccess) return hip_fail(e, "hipDeviceGetAttribute(LDS per CU)");
+    DeviceInfo d;
+    d.gfx950 = strncmp(prop.gcnArchName, "gfx950", 6) == 0;
+    d.batch_lds = batch_lds_bytes(static_cast<size_t>(lds));
+    it = known.emplace(dev, d).first;
+  }
+  if (!it->second.gfx950)
+    return fail(ZERO_ERR_UNSUPPORTED, "device %d is not gfx950, the target this library is built for", dev);
+  if (info) *info = it->second;
+  return ZERO_OK;
+}
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+// Reduce the `blocks` partials a launch just wrote into the level-2 partials
+// of group g (the launchers report their grid size, or 0 when a small launch
+// wrote the level-2 partials itself: then there is nothing to fold).
+hipError_t fold_into(void* ws, int32_t g, int64_t blocks, hipStream_t s) {
+  if (blocks == 0) return hipSuccess;
+  FoldArgs F;
+  F.partials = scratch_of(ws);
+  F.count = blocks;
+  F.level2 = level2_of(ws, g);
+  return launch_fold(F, s);
+}
+
+int check_workspace(const void* ws, size_t have) {
+  if (!ws) return fail(ZERO_ERR_WORKSPACE, "workspace is NULL");
+  if (!aligned(ws, 256)) return fail(ZERO_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+  if (have < kWorkspaceBytes)
+    return fail(ZERO_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu needed", have, kWorkspaceBytes);
+  return ZERO_OK;
+}
+
+}  // namespace zdp
+
+namespace {
+
+bool valid_dt(int32_t dt) { return dt == ZERO_DT_F16 || dt == ZERO_DT_BF16; }
 
 // Largest of 8/4/2 dividing the address (the widest 16-bit store is 8 bytes).
 int32_t align_class(const void* p) {
@@ -70,63 +121,6 @@ class HeadCheck {
   static constexpr int64_t kUnset = -2, kMixed = -1;
   int64_t h_ = kUnset;
 };
-
-// What the launches need to know of a device, found once per device.
-struct DeviceInfo {
-  bool gfx950;
-  size_t batch_lds;  // dynamic LDS per block of the batched update schedule
-};
-
-// The current device must be gfx950. *info (optional) receives its DeviceInfo.
-int check_device(DeviceInfo* info = nullptr) {
-  static std::mutex mu;
-  static std::unordered_map<int, DeviceInfo> known;
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
-  std::lock_guard<std::mutex> lk(mu);
-  auto it = known.find(dev);
-  if (it == known.end()) {
-    hipDeviceProp_t prop;
-    e = hipGetDeviceProperties(&prop, dev);
-    if (e != hipSuccess) return hip_fail(e, "hipGetDeviceProperties");
-    int lds = 0;
-    e = hipDeviceGetAttribute(&lds, hipDeviceAttributeMaxSharedMemoryPerMultiprocessor, dev);
-    if (e != hipSuccess) return hip_fail(e, "hipDeviceGetAttribute(LDS per CU)");
-    DeviceInfo d;
-    d.gfx950 = strncmp(prop.gcnArchName, "gfx950", 6) == 0;
-    d.batch_lds = batch_lds_bytes(static_cast<size_t>(lds));
-    it = known.emplace(dev, d).first;
-  }
-  if (!it->second.gfx950)
-    return fail(ZERO_ERR_UNSUPPORTED, "device %d is not gfx950, the target this library is built for", dev);
-  if (info) *info = it->second;
-  return ZERO_OK;
-}
-
-// Workspace: per-group level-2 partials, then the block partials of the latest launch.
-double* level2_of(void* ws, int32_t g) { return static_cast<double*>(ws) + static_cast<int64_t>(g) * kFoldBlocks; }
-double* scratch_of(void* ws) { return reinterpret_cast<double*>(static_cast<char*>(ws) + kHeaderBytes); }
-
-// Reduce the `blocks` partials a launch just wrote into the level-2 partials
-// of group g (the launchers report their grid size, or 0 when a small launch
-// wrote the level-2 partials itself: then there is nothing to fold).
-hipError_t fold_into(void* ws, int32_t g, int64_t blocks, hipStream_t s) {
-  if (blocks == 0) return hipSuccess;
-  FoldArgs F;
-  F.partials = scratch_of(ws);
-  F.count = blocks;
-  F.level2 = level2_of(ws, g);
-  return launch_fold(F, s);
-}
-
-int check_workspace(const void* ws, size_t have) {
-  if (!ws) return fail(ZERO_ERR_WORKSPACE, "workspace is NULL");
-  if (!aligned(ws, 256)) return fail(ZERO_ERR_WORKSPACE, "workspace is not 256-byte aligned");
-  if (have < kWorkspaceBytes)
-    return fail(ZERO_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu needed", have, kWorkspaceBytes);
-  return ZERO_OK;
-}
 
 int check_policy(const zero_policy* p) {
   if (!p) return ZERO_OK;
