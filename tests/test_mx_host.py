@@ -144,13 +144,15 @@ def test_binding_refuses_host_tensors():
 
 
 def test_binding_row_checks():
-    dev = torch.device("cpu")
+    dev = -1  # the host
     f = zdp._need_rows
     x = torch.zeros(6, 10)
     types = zdp._mx_types()
-    assert f(x, "x", types, dev) == 10
-    assert f(x[:, 2:7], "x", types, dev) == 10
-    assert f(x[1:2], "x", types, dev) == 10
+    assert f(x, "x", types, dev) == (6, 10, 10)
+    assert f(x[:, 2:7], "x", types, dev) == (6, 5, 10)
+    assert f(x[1:2], "x", types, dev) == (1, 10, 10)
+    with pytest.raises(ValueError, match="expected device 0"):
+        f(x, "x", types, 0)
     with pytest.raises(ValueError, match="not dense"):
         f(x.t(), "x", types, dev)
     with pytest.raises(ValueError, match="overlap"):
@@ -164,11 +166,11 @@ def test_binding_row_checks():
 
 
 def test_binding_matrix_checks():
-    dev = torch.device("cpu")
+    dev = -1
     c, s = _mx_tensors(6, 4)
     f = zdp._need_mx
-    assert f(c, s, "A", dev, 6, 97) == 4
-    assert f(c[:, 16:48], s[:, 1:3], "A", dev, 6, 64) == 4
+    assert f(c, s, "A", dev, 6, 97) == (6, 4, 4)
+    assert f(c[:, 16:48], s[:, 1:3], "A", dev, 6, 64) == (6, 2, 4)
     with pytest.raises(ValueError, match="blocks a row"):
         f(c, s, "A", dev, 6, 96)
     with pytest.raises(ValueError, match="rows"):
@@ -182,11 +184,11 @@ def test_binding_matrix_checks():
 
 
 def test_binding_flat_checks():
-    dev = torch.device("cpu")
+    dev = -1
     c, s = torch.zeros(16 * 5, dtype=torch.uint8), torch.zeros(5, dtype=torch.uint8)
     f = zdp._need_flat
-    assert f(c, s, "v", dev, 64, 96) == 5
-    assert f(c, s, "v", dev, 64, 70) == 5
+    assert f(c, s, "v", dev, 64, 96) == (5, 5)
+    assert f(c, s, "v", dev, 64, 70) == (5, 5)
     for offset, n in ((64, 97), (32 * 5, 1), (33, 1), (-32, 32)):
         with pytest.raises(ValueError):
             f(c, s, "v", dev, offset, n)

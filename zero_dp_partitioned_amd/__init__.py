@@ -551,78 +551,105 @@ def mx_view(codes, scales, offset, rows, cols):
     return (codes[16 * b:16 * (b + n)].view(rows, cols // 2), scales[b:b + n].view(rows, cols // MX_BLOCK))
 
 
+_MX_DT = {}
+
+
 def _mx_types():
-    torch = _torch()
-    return (torch.float32, torch.float16, torch.bfloat16)
+    """Value dtypes of the 4-bit calls and their codes (torch is imported on first use)."""
+    if not _MX_DT:
+        torch = _torch()
+        _MX_DT.update({torch.float32: DT_F32, torch.float16: DT_F16, torch.bfloat16: DT_BF16})
+    return _MX_DT
 
 
-def _mx_dt(t):
-    return DT_F32 if t.dtype == _torch().float32 else _dt(t)
-
-
-def _on(device):
-    """The device context and the stream argument of a call on `device`'s
-    tensors (its current stream unless the caller names one)."""
-    return _torch().cuda.device(device)
+def _u8():
+    return (_torch().uint8,)
 
 
 def _device_of(t, name):
+    """The index of the device a tensor is on."""
     torch = _torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    return t.device
+    return t.get_device()
+
+
+def _call(fn, device, stream, *args):
+    """Call an entry point on `device`'s current stream (or the one given), with that device current."""
+    torch = _torch()
+    s = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == device:
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, s)
+    if rc != OK:
+        raise ZeroError(rc, last_error())
 
 
 def _need_rows(t, name, dtypes, device):
-    """A 2-D tensor of one of `dtypes` on `device` with dense rows; the elements from row to row."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+    """(rows, cols, elements from row to row) of a 2-D tensor of one of `dtypes` on `device` (an index, -1 for the
+    host) with dense rows."""
+    if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name}: a torch tensor is expected, got {type(t).__name__}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
-    if t.device != device:
-        raise ValueError(f"{name}: tensor on {t.device}, expected {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: tensor on {t.device}, expected device {device}")
     if t.dim() != 2:
         raise ValueError(f"{name}: {t.dim()} dimensions, expected 2")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1:
         raise ValueError(f"{name}: its rows are not dense")
     if rows <= 1:
-        return max(1, cols)
-    if t.stride(0) < cols:
+        return rows, cols, cols
+    if s0 < cols:
         raise ValueError(f"{name}: rows overlap")
-    return t.stride(0)
+    return rows, cols, s0
 
 
 def _need_mx(codes, scales, name, device, rows=None, values=None):
-    """A 4-bit matrix (2-D codes and scales); its blocks from row to row."""
-    u8 = (_torch().uint8,)
-    ld_c = _need_rows(codes, f"{name} codes", u8, device)
-    ld_s = _need_rows(scales, f"{name} scales", u8, device)
-    r, kb = scales.shape
-    if tuple(codes.shape) != (r, 16 * kb):
-        raise ValueError(f"{name}: codes {tuple(codes.shape)} do not match scales {tuple(scales.shape)}: "
-                         f"expected {(r, 16 * kb)}")
+    """(rows, blocks a row, blocks from row to row) of a 4-bit matrix (2-D codes and scales)."""
+    u8 = _u8()
+    rc, cc, ld_c = _need_rows(codes, name, u8, device)
+    r, kb, ld = _need_rows(scales, name, u8, device)
+    if rc != r or cc != 16 * kb:
+        raise ValueError(f"{name}: codes {(rc, cc)} do not match scales {(r, kb)}: expected {(r, 16 * kb)}")
     if rows is not None and r != rows:
         raise ValueError(f"{name}: {r} rows, expected {rows}")
     if values is not None and kb != -(-values // MX_BLOCK):
         raise ValueError(f"{name}: {kb} blocks a row, expected {-(-values // MX_BLOCK)}")
-    if r > 1 and kb > 0 and ld_c != 16 * ld_s:
-        raise ValueError(f"{name}: rows of codes lie {ld_c} bytes apart and rows of scales {ld_s}: expected 16 to 1")
-    return max(ld_s, kb)
+    if ld_c != 16 * ld and kb > 0:
+        raise ValueError(f"{name}: rows of codes lie {ld_c} bytes apart and rows of scales {ld}: expected 16 to 1")
+    return r, kb, ld
+
+
+def _need_values(t, name, dtypes, device):
+    """The length of a dense tensor of one of `dtypes` on `device` (an index)."""
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name}: a torch tensor is expected, got {type(t).__name__}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: tensor on {t.device}, expected device {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    return t.numel()
 
 
 def _need_flat(codes, scales, name, device, offset, n):
-    """A flat 4-bit vector that holds elements [offset, offset + n)."""
-    u8 = (_torch().uint8,)
-    _need(codes, f"{name} codes", u8, device)
-    _need(scales, f"{name} scales", u8, device)
+    """The last block (exclusive) of elements [offset, offset + n) of a flat 4-bit vector that holds them, and its
+    blocks."""
+    u8 = _u8()
+    nbytes = _need_values(codes, name, u8, device)
+    blocks = _need_values(scales, name, u8, device)
     if offset < 0 or offset % MX_BLOCK:
         raise ValueError(f"{name}: offset {offset} is not a multiple of {MX_BLOCK}")
     end = offset // MX_BLOCK + -(-n // MX_BLOCK)
-    if scales.numel() < end or codes.numel() < 16 * end:
+    if blocks < end or nbytes < 16 * end:
         raise ValueError(f"{name}: offset + n exceeds the flat vector")
-    return end
+    return end, blocks
 
 
 def mx_cast_writeback(master, codes, scales, offset=0, stream=None):
@@ -630,13 +657,11 @@ def mx_cast_writeback(master, codes, scales, offset=0, stream=None):
     of 32). A shard that ends inside a block must end the vector: the block's
     other values would belong to the next rank."""
     dev = _device_of(master, "master")
-    _need(master, "master", _f32(), dev)
-    n = master.numel()
-    end = _need_flat(codes, scales, "flat vector", dev, offset, n)
-    if n % MX_BLOCK and end != scales.numel():
+    n = _need_values(master, "master", _f32(), dev)
+    end, blocks = _need_flat(codes, scales, "flat vector", dev, offset, n)
+    if n % MX_BLOCK and end != blocks:
         raise ValueError(f"a shard of {n} values ends inside a block that is not the vector's last one")
-    with _on(dev):
-        _check(load().zero_mx_cast_writeback(_ptr(master), n, _ptr(codes), _ptr(scales), offset, _stream(stream)))
+    _call(load().zero_mx_cast_writeback, dev, stream, master.data_ptr(), n, codes.data_ptr(), scales.data_ptr(), offset)
 
 
 def mx_quantize(src, codes=None, scales=None, codes_t=None, scales_t=None, stream=None):
@@ -644,17 +669,22 @@ def mx_quantize(src, codes=None, scales=None, codes_t=None, scales_t=None, strea
     and / or along its columns into (codes_t, scales_t), the transposed matrix;
     allocate them with mx_empty(rows, cols) and mx_empty(cols, rows)."""
     dev = _device_of(src, "src")
-    src_ld = _need_rows(src, "src", _mx_types(), dev)
-    rows, cols = src.shape
+    types = _mx_types()
+    rows, cols, src_ld = _need_rows(src, "src", types, dev)
     if (codes is None) != (scales is None) or (codes_t is None) != (scales_t is None):
         raise ValueError("codes and scales must be given together")
-    if codes is None and codes_t is None:
+    c = s = ct = st = None
+    ld = ld_t = 0
+    if codes is not None:
+        ld = _need_mx(codes, scales, "output", dev, rows, cols)[2]
+        c, s = codes.data_ptr(), scales.data_ptr()
+    if codes_t is not None:
+        ld_t = _need_mx(codes_t, scales_t, "transposed output", dev, cols, rows)[2]
+        ct, st = codes_t.data_ptr(), scales_t.data_ptr()
+    elif codes is None:
         raise ValueError("no output")
-    ld = _need_mx(codes, scales, "output", dev, rows, cols) if codes is not None else 0
-    ld_t = _need_mx(codes_t, scales_t, "transposed output", dev, cols, rows) if codes_t is not None else 0
-    with _on(dev):
-        _check(load().zero_mx_quantize(_ptr(src), _mx_dt(src), rows, cols, src_ld, _ptr(codes), _ptr(scales), ld,
-                                       _ptr(codes_t), _ptr(scales_t), ld_t, _stream(stream)))
+    _call(load().zero_mx_quantize, dev, stream, src.data_ptr(), types[src.dtype], rows, cols, src_ld, c, s, ld, ct, st,
+          ld_t)
 
 
 def mx_dequantize(codes, scales, out, offset=0, stream=None):
@@ -662,38 +692,33 @@ def mx_dequantize(codes, scales, out, offset=0, stream=None):
     [offset, offset + out.numel()) of a flat 4-bit vector (1-D), in out's dtype
     (fp32, fp16 or bf16)."""
     dev = _device_of(out, "out")
+    types = _mx_types()
     if out.dim() == 1:
-        _need(out, "out", _mx_types(), dev)
-        rows, cols = 1, out.numel()
+        rows, cols = 1, _need_values(out, "out", types, dev)
         _need_flat(codes, scales, "flat vector", dev, offset, cols)
-        b = offset // MX_BLOCK
-        cp, sp = ctypes.c_void_p(codes.data_ptr() + 16 * b), ctypes.c_void_p(scales.data_ptr() + b)
         ld, out_ld = -(-cols // MX_BLOCK), cols
     else:
         if offset:
             raise ValueError("offset is for flat vectors")
-        out_ld = _need_rows(out, "out", _mx_types(), dev)
-        rows, cols = out.shape
-        ld = _need_mx(codes, scales, "input", dev, rows, cols)
-        cp, sp = _ptr(codes), _ptr(scales)
-    with _on(dev):
-        _check(load().zero_mx_dequantize(cp, sp, rows, cols, ld, _ptr(out), _mx_dt(out), out_ld, _stream(stream)))
+        rows, cols, out_ld = _need_rows(out, "out", types, dev)
+        ld = _need_mx(codes, scales, "input", dev, rows, cols)[2]
+    b = offset // MX_BLOCK
+    _call(load().zero_mx_dequantize, dev, stream, codes.data_ptr() + 16 * b, scales.data_ptr() + b, rows, cols, ld,
+          out.data_ptr(), types[out.dtype], out_ld)
 
 
 def mx_reduce_grad_segment(codes, scales, avg_out, workspace, group, state, stream=None):
     """reduce_grad_segment over copies in 4 bits: codes and scales are lists of
     N_d flat vectors (1-D uint8), each holding the segment from element 0."""
-    dev = _state_device(state, workspace)
-    _need(avg_out, "avg_out", _f32(), dev)
-    n = avg_out.numel()
-    if not codes or len(codes) != len(scales):
-        raise ValueError(f"{len(codes)} copies of codes and {len(scales)} of scales")
-    for r, (c, s) in enumerate(zip(codes, scales)):
-        _need_flat(c, s, f"copy {r}", dev, 0, n)
-    with _on(dev):
-        _check(load().zero_mx_reduce_grad_segment(_ptr_array(codes), _ptr_array(scales), len(codes), n, _ptr(avg_out),
-                                                  _ptr(workspace), _nbytes(workspace), group, _ptr(state),
-                                                  _stream(stream)))
+    dev = _state_device(state, workspace).index
+    n = _need_values(avg_out, "avg_out", _f32(), dev)
+    n_d = len(codes)
+    if not n_d or n_d != len(scales):
+        raise ValueError(f"{n_d} copies of codes and {len(scales)} of scales")
+    for r in range(n_d):
+        _need_flat(codes[r], scales[r], f"copy {r}", dev, 0, n)
+    _call(load().zero_mx_reduce_grad_segment, dev, stream, _ptr_array(codes), _ptr_array(scales), n_d, n,
+          avg_out.data_ptr(), workspace.data_ptr(), _nbytes(workspace), group, state.data_ptr())
 
 
 def mx_product(a_codes, a_scales, b_codes, b_scales, out, stream=None):
@@ -702,13 +727,11 @@ def mx_product(a_codes, a_scales, b_codes, b_scales, out, stream=None):
     layer: y = x W^T takes x and W, dx = dy W takes dy and W's transposed copy,
     dW = dy^T x takes the transposed copies of dy and x (mx_quantize)."""
     dev = _device_of(out, "out")
-    ldo = _need_rows(out, "out", _mx_types(), dev)
-    m, n = out.shape
-    lda = _need_mx(a_codes, a_scales, "A", dev, m)
-    ldb = _need_mx(b_codes, b_scales, "B", dev, n)
-    kb = a_scales.shape[1]
-    if b_scales.shape[1] != kb:
-        raise ValueError(f"A has {kb} blocks a row, B {b_scales.shape[1]}")
-    with _on(dev):
-        _check(load().zero_mx_product(_ptr(a_codes), _ptr(a_scales), lda, _ptr(b_codes), _ptr(b_scales), ldb, m, n, kb,
-                                      _ptr(out), _mx_dt(out), max(ldo, n), _stream(stream)))
+    types = _mx_types()
+    m, n, ldo = _need_rows(out, "out", types, dev)
+    _, kb, lda = _need_mx(a_codes, a_scales, "A", dev, m)
+    _, kb_b, ldb = _need_mx(b_codes, b_scales, "B", dev, n)
+    if kb_b != kb:
+        raise ValueError(f"A has {kb} blocks a row, B {kb_b}")
+    _call(load().zero_mx_product, dev, stream, a_codes.data_ptr(), a_scales.data_ptr(), lda, b_codes.data_ptr(),
+          b_scales.data_ptr(), ldb, m, n, kb, out.data_ptr(), types[out.dtype], ldo)

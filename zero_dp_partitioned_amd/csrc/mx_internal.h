@@ -17,6 +17,7 @@ constexpr int kMxCodeBytes = 16;   // bytes of codes in a block
 constexpr int kMxNaN = 255;        // the scale byte of a block that holds inf or NaN
 
 inline int64_t mx_blocks(int64_t values) { return values / kMxBlock + (values % kMxBlock != 0); }
+inline int64_t mx_tiles(int64_t n, int64_t size) { return n / size + (n % size != 0); }
 
 struct MxQuantArgs {
   const void* src;  // rows x cols values of src_dt, `src_ld` values from row to row

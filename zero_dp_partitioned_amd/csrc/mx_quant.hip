@@ -91,36 +91,117 @@ __global__ void __launch_bounds__(kBlock) mx_quantize_rows_kernel(const MxQuantA
 }
 
 // ------------------------------------------------------------------------
-// Quantise along the columns (the transpose's rows): item i is quarter i % 4
-// of block i / 4, blocks counted column by column.
+// Quantise along the columns (the transpose's rows) and, if wanted, along the
+// rows from the same read. A block takes a tile of 128 x 128 values: it reads
+// them row by row as the row kernel does (and quantises the rows), keeps them
+// in LDS in their own type, and then takes every column's four blocks of 32
+// from there. 128 values either way make a tile's codes 64 contiguous bytes of
+// every row and of every column.
+// LDS holds rows of dwords (two 16-bit values or one fp32 value each); dword c
+// of row i stands at c ^ 16 * (i / 32). A wave's column reads take 16
+// neighbouring dwords of four rows that are 32 rows apart, and the permutation
+// puts those four runs into different banks.
 // ------------------------------------------------------------------------
 
+constexpr int kSide = 128;                     // values of a tile, either way
+constexpr int kSideLanes = kSide / kLane;      // lanes that read a row
+constexpr int kPasses = kSide / (kBlock / kSideLanes);
+constexpr int kStrip = 4;                      // tiles next to each other that are worked on in turn
+
 template <int DT>
-__global__ void __launch_bounds__(kBlock) mx_quantize_cols_kernel(const MxQuantArgs Q) {
-  const int64_t rb = (Q.rows + kMxBlock - 1) / kMxBlock;
-  const int64_t items = Q.cols * rb * kLanesPerBlock;
-  for (int64_t t0 = blockIdx.x * static_cast<int64_t>(kBlock); t0 < items; t0 += static_cast<int64_t>(gridDim.x) * kBlock) {
-    const int64_t i = t0 + threadIdx.x;
-    const int64_t b = i / kLanesPerBlock;
-    const int64_t col = b / rb, br = b - col * rb;
-    const int64_t e = br * kMxBlock + (i % kLanesPerBlock) * kLane;
-    float v[8];
+__global__ void __launch_bounds__(kBlock) mx_quantize_tile_kernel(const MxQuantArgs Q) {
+  constexpr int kElem = DT == ZERO_DT_F32 ? 4 : 2;
+  constexpr int kDwords = kSide * kElem / 4;  // of a row
+  constexpr int kPer = 4 / kElem;             // columns in a dword
+  __shared__ __align__(16) uint32_t tile[kSide * kDwords];
+  const int64_t tr = (Q.rows + kSide - 1) / kSide, tc = (Q.cols + kSide - 1) / kSide;
+  const int64_t tiles = tr * tc;
+  const int tid = threadIdx.x;
+  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+    // strips of kStrip tile columns, row by row: the halves of a line of codes
+    // and the pieces of a line of scales are written soon after one another
+    const int64_t strip = t / (tr * kStrip), at = t - strip * tr * kStrip;
+    const int64_t wide = tc - strip * kStrip < kStrip ? tc - strip * kStrip : kStrip;
+    const int64_t r0 = at / wide * kSide, c0 = (strip * kStrip + at % wide) * kSide;
+    const int64_t e = c0 + (tid % kSideLanes) * kLane;
+    float v[kPasses][8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      float one[8] = {};
-      if (i < items && e + q < Q.rows) {
-        const int elem = DT == ZERO_DT_F32 ? 4 : 2;
-        load8<DT>(static_cast<const char*>(Q.src) + (e + q) * Q.src_ld * elem, col, 1, one);
+    for (int p = 0; p < kPasses; ++p) {
+      const int64_t row = r0 + p * (kBlock / kSideLanes) + tid / kSideLanes;
+      load8<DT>(static_cast<const char*>(Q.src) + row * Q.src_ld * kElem, e, row < Q.rows ? Q.cols - e : 0, v[p]);
+    }
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      const int i = p * (kBlock / kSideLanes) + tid / kSideLanes;
+      uint32_t* const to = tile + i * kDwords;
+      const int first = (tid % kSideLanes) * kLane / kPer;
+      if constexpr (DT == ZERO_DT_F32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const f4 x = {v[p][4 * h], v[p][4 * h + 1], v[p][4 * h + 2], v[p][4 * h + 3]};
+          *reinterpret_cast<f4*>(to + ((first + 4 * h) ^ (i / 32 * 16))) = x;
+        }
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          // the 16-bit patterns again (the conversion to fp32 lost nothing)
+          if constexpr (DT == ZERO_DT_BF16) {
+            w[q] = (__float_as_uint(v[p][2 * q]) >> 16) | (__float_as_uint(v[p][2 * q + 1]) & 0xFFFF0000u);
+          } else {
+            const h2 h = {static_cast<_Float16>(v[p][2 * q]), static_cast<_Float16>(v[p][2 * q + 1])};
+            w[q] = __builtin_bit_cast(uint32_t, h);
+          }
+        }
+        *reinterpret_cast<u4*>(to + (first ^ (i / 32 * 16))) = (u4){w[0], w[1], w[2], w[3]};
       }
-      v[q] = one[0];
+      if (Q.codes) {
+        const uint32_t byte = scale_byte(quad_max(max_bits8(v[p])));
+        const uint32_t c = encode8(v[p], byte);
+        if (r0 + i < Q.rows && e / kMxBlock * kMxBlock < Q.cols) {
+          const int64_t b = (r0 + i) * Q.ld + e / kMxBlock;
+          reinterpret_cast<uint32_t*>(Q.codes)[b * 4 + tid % 4] = c;
+          if (tid % 4 == 0) Q.scales[b] = static_cast<uint8_t>(byte);
+        }
+      }
     }
-    const uint32_t byte = scale_byte(quad_max(max_bits8(v)));
-    const uint32_t c = encode8(v, byte);
-    if (i < items) {
-      const int64_t at = col * Q.ld_t + br;
-      reinterpret_cast<uint32_t*>(Q.codes_t)[at * 4 + i % kLanesPerBlock] = c;
-      if (i % kLanesPerBlock == 0) Q.scales_t[at] = static_cast<uint8_t>(byte);
+    __syncthreads();
+    const int rb = tid % 4;  // the column's block of 32
+#pragma unroll
+    for (int h = 0; h < 2 / kPer; ++h) {
+      const int d = h * 64 + tid / 4;  // the dword: kPer columns
+      float x[kPer][kMxBlock];
+#pragma unroll
+      for (int q = 0; q < kMxBlock; ++q) {
+        const uint32_t w = tile[(rb * kMxBlock + q) * kDwords + (d ^ (rb * 16))];
+        if constexpr (DT == ZERO_DT_F32) {
+          x[0][q] = __uint_as_float(w);
+        } else {
+          constexpr int K = DT == ZERO_DT_BF16 ? kSrcBF16 : kSrcF16;
+          x[0][q] = decode16<K>(w & 0xFFFFu);
+          x[kPer - 1][q] = decode16<K>(w >> 16);
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < kPer; ++y) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int q = 0; q < kMxBlock; q += 8) {
+          const uint32_t n = max_bits8(&x[y][q]);
+          m = n > m ? n : m;
+        }
+        const uint32_t byte = scale_byte(m);
+        const u4 c = {encode8(&x[y][0], byte), encode8(&x[y][8], byte), encode8(&x[y][16], byte),
+                      encode8(&x[y][24], byte)};
+        const int64_t col = c0 + d * kPer + y;
+        if (col < Q.cols && r0 + rb * kMxBlock < Q.rows) {
+          const int64_t b = col * Q.ld_t + r0 / kMxBlock + rb;
+          *reinterpret_cast<u4*>(Q.codes_t + b * kMxCodeBytes) = c;
+          Q.scales_t[b] = static_cast<uint8_t>(byte);
+        }
+      }
     }
+    __syncthreads();
   }
 }
 
@@ -208,6 +289,36 @@ __global__ void __launch_bounds__(kBlock) mx_widen_kernel(const MxWidenArgs W) {
 // gradient (as the 16-bit averaging pass).
 // ------------------------------------------------------------------------
 
+// Groups of 8 values a lane has in flight, and copies whose loads it issues at
+// a time (the additions stay in the copies' order).
+constexpr int kReduceGroups = 2;
+constexpr int kReduceCopies = 8;
+
+template <int N>
+__device__ __forceinline__ void add_copies(const MxCopies& S, int r, const int64_t at[kReduceGroups],
+                                           float acc[kReduceGroups][8]) {
+  uint32_t c[N][kReduceGroups], e[N][kReduceGroups];
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const uint8_t* codes = S.strided ? S.codes[0] + (r + q) * S.code_stride : S.codes[r + q];
+    const uint8_t* scales = S.strided ? S.scales[0] + (r + q) * S.scale_stride : S.scales[r + q];
+#pragma unroll
+    for (int k = 0; k < kReduceGroups; ++k) {
+      c[q][k] = ld_stream(reinterpret_cast<const uint32_t*>(codes) + at[k]);
+      e[q][k] = scales[at[k] / kLanesPerBlock];
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < N; ++q)
+#pragma unroll
+    for (int k = 0; k < kReduceGroups; ++k) {
+      float v[8];
+      decode8(c[q][k], scale_operand(e[q][k]), v);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) acc[k][x] = acc[k][x] + v[x];
+    }
+}
+
 __global__ void __launch_bounds__(kBlock) mx_reduce_kernel(const MxReduceArgs R) {
   const float inv_scale = static_cast<float>(1.0 / static_cast<double>(R.state->loss_scale));
   double sumsq = 0.0;
@@ -215,25 +326,40 @@ __global__ void __launch_bounds__(kBlock) mx_reduce_kernel(const MxReduceArgs R)
   const int64_t n = R.n;
   const int64_t items = (n + kLane - 1) / kLane;
   const MxCopies& S = R.src;
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(kBlock) + threadIdx.x; i < items;
-       i += static_cast<int64_t>(gridDim.x) * kBlock) {
-    float acc[8] = {};
-    for (int r = 0; r < S.n_d; ++r) {
-      const uint8_t* codes = S.strided ? S.codes[0] + r * S.code_stride : S.codes[r];
-      const uint8_t* scales = S.strided ? S.scales[0] + r * S.scale_stride : S.scales[r];
-      float v[8];
-      decode8(reinterpret_cast<const uint32_t*>(codes)[i], scale_operand(scales[i / kLanesPerBlock]), v);
+  constexpr int64_t T = static_cast<int64_t>(kBlock) * kReduceGroups;
+  for (int64_t t0 = blockIdx.x * T; t0 < items; t0 += gridDim.x * T) {
+    float acc[kReduceGroups][8] = {};
+    int64_t at[kReduceGroups];  // past the end: the last item again
 #pragma unroll
-      for (int q = 0; q < 8; ++q) acc[q] = acc[q] + v[q];
+    for (int k = 0; k < kReduceGroups; ++k) {
+      const int64_t i = t0 + k * kBlock + threadIdx.x;
+      at[k] = i < items ? i : items - 1;
     }
-    const int64_t e = i * kLane;
-    const int64_t left = n - e;
+    int r = 0;
+    for (; r + kReduceCopies <= S.n_d; r += kReduceCopies) add_copies<kReduceCopies>(S, r, at, acc);
+    if (r + 4 <= S.n_d) { add_copies<4>(S, r, at, acc); r += 4; }
+    if (r + 2 <= S.n_d) { add_copies<2>(S, r, at, acc); r += 2; }
+    if (r < S.n_d) add_copies<1>(S, r, at, acc);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      if (q >= left) continue;
-      const float a = S.n_d == 1 ? acc[q] : (S.inv_nd != 0.0f ? acc[q] * S.inv_nd : acc[q] / S.nd);
-      account(a, a * inv_scale, sumsq, bad);
-      R.avg_out[e + q] = a;
+    for (int k = 0; k < kReduceGroups; ++k) {
+      const int64_t e = (t0 + k * kBlock + threadIdx.x) * kLane;
+      const int64_t left = n - e;
+      float a[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        a[q] = S.n_d == 1 ? acc[k][q] : (S.inv_nd != 0.0f ? acc[k][q] * S.inv_nd : acc[k][q] / S.nd);
+        if (q < left) account(a[q], a[q] * inv_scale, sumsq, bad);
+      }
+      float* const p = R.avg_out + e;
+      if (left >= 8) {
+        const f4 x = {a[0], a[1], a[2], a[3]}, y = {a[4], a[5], a[6], a[7]};
+        __builtin_memcpy(p, &x, 16);
+        __builtin_memcpy(p + 4, &y, 16);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (q < left) p[q] = a[q];
+      }
     }
   }
   write_block_partial(sumsq, bad, R.partials, R.fill);
@@ -247,22 +373,19 @@ int mx_grid(int64_t items, int64_t per_block) {
 
 template <int DT>
 hipError_t quantize_launch(const MxQuantArgs& a, hipStream_t s) {
-  if (a.codes) {
-    MxQuantArgs q = a;
-    if (q.cols % kMxBlock == 0 && q.src_ld == q.cols && q.ld == q.cols / kMxBlock) {
-      q.cols *= q.rows;  // one long row
-      q.rows = 1;
-    }
-    const int64_t items = q.rows * mx_blocks(q.cols) * kLanesPerBlock;
-    hipLaunchKernelGGL((mx_quantize_rows_kernel<DT>), dim3(mx_grid(items, kBlock * kMxGroups)), dim3(kBlock), 0, s, q);
-    if (hipError_t e = hipGetLastError()) return e;
-  }
   if (a.codes_t) {
-    const int64_t items = a.cols * mx_blocks(a.rows) * kLanesPerBlock;
-    hipLaunchKernelGGL((mx_quantize_cols_kernel<DT>), dim3(mx_grid(items, kBlock)), dim3(kBlock), 0, s, a);
-    if (hipError_t e = hipGetLastError()) return e;
+    const int64_t tiles = mx_tiles(a.rows, kSide) * mx_tiles(a.cols, kSide);
+    hipLaunchKernelGGL((mx_quantize_tile_kernel<DT>), dim3(mx_grid(tiles, 1)), dim3(kBlock), 0, s, a);
+    return hipGetLastError();
   }
-  return hipSuccess;
+  MxQuantArgs q = a;
+  if (q.cols % kMxBlock == 0 && q.src_ld == q.cols && q.ld == q.cols / kMxBlock) {
+    q.cols *= q.rows;  // one long row
+    q.rows = 1;
+  }
+  const int64_t items = q.rows * mx_blocks(q.cols) * kLanesPerBlock;
+  hipLaunchKernelGGL((mx_quantize_rows_kernel<DT>), dim3(mx_grid(items, kBlock * kMxGroups)), dim3(kBlock), 0, s, q);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -289,7 +412,7 @@ hipError_t launch_mx_widen(const MxWidenArgs& args, int32_t dt, hipStream_t s) {
 }
 
 hipError_t launch_mx_reduce(const MxReduceArgs& args, hipStream_t s, int* blocks) {
-  const int grid = mx_grid((args.n + kLane - 1) / kLane, kBlock);
+  const int grid = mx_grid((args.n + kLane - 1) / kLane, kBlock * kReduceGroups);
   const MxReduceArgs a = route_partials(args, grid, blocks);
   hipLaunchKernelGGL(mx_reduce_kernel, dim3(grid), dim3(kBlock), 0, s, a);
   return hipGetLastError();
