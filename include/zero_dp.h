@@ -82,6 +82,7 @@ extern "C" {
  *   kept. A block that holds inf or NaN becomes a NaN block (byte 255, codes 0).
  * Alignment: codes 16 bytes, scales any, values their own size. */
 #define ZERO_MX_BLOCK 32
+#define ZERO_MX_MAX_LD 1048575 /* zero_mx_product: blocks from row to row */
 
 /* One rank's segment of a flat vector: elements [offset, offset + size). */
 typedef struct {
@@ -428,7 +429,8 @@ int zero_mx_reduce_grad_segment(const void* const* codes, const void* const* sca
  * dx = dy W from dy and the transposed copy of W, dW = dy^T x from the
  * transposed copies of dy and x.
  * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (more than 2^31 - 1 rows in A or
- * B, or output tiles past a launch's limit). */
+ * B, rows more than ZERO_MX_MAX_LD blocks apart, or output tiles past a
+ * launch's limit). */
 int zero_mx_product(const void* a_codes, const void* a_scales, int64_t lda, const void* b_codes, const void* b_scales,
                     int64_t ldb, int64_t m, int64_t n, int64_t k_blocks, void* out, int32_t out_dt, int64_t ldo,
                     void* stream);

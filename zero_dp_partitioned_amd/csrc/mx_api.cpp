@@ -176,6 +176,8 @@ int zero_mx_product(const void* a_codes, const void* a_scales, int64_t lda, cons
   if (int rc = check_mx("B", b_codes, b_scales, n, k_blocks, ldb)) return rc;
   if (int rc = check_values("out", out, out_dt, m, n, ldo)) return rc;
   if (m == 0 || n == 0) return ZERO_OK;
+  if (lda > kMxMaxLd || ldb > kMxMaxLd)
+    return fail(ZERO_ERR_UNSUPPORTED, "rows more than %lld blocks apart", (long long)kMxMaxLd);
   if ((m + 31) / 32 * ((n + 31) / 32) > INT32_MAX) return fail(ZERO_ERR_UNSUPPORTED, "too many output tiles");
   if (int rc = check_device()) return rc;
   MxProductArgs P;

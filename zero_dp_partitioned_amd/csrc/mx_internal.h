@@ -16,6 +16,11 @@ constexpr int kMxBlock = 32;       // values that share a scale
 constexpr int kMxCodeBytes = 16;   // bytes of codes in a block
 constexpr int kMxNaN = 255;        // the scale byte of a block that holds inf or NaN
 
+// Blocks from row to row of a product's operand: the byte offsets inside a tile
+// of 256 rows are 32-bit.
+constexpr int64_t kMxMaxLd = ZERO_MX_MAX_LD;
+static_assert((256 * kMxMaxLd) * kMxCodeBytes < (int64_t{1} << 32), "offsets of a tile");
+
 inline int64_t mx_blocks(int64_t values) { return values / kMxBlock + (values % kMxBlock != 0); }
 inline int64_t mx_tiles(int64_t n, int64_t size) { return n / size + (n % size != 0); }
 

@@ -28,15 +28,19 @@ constexpr int kFrag = 32;    // rows of an operand per instruction
 // scales of a lane's blocks of the chunk, step s in byte 2 * (s & 1) of dword
 // s >> 1 (chunk_scales).
 template <int S>
-__device__ __forceinline__ v16f mfma(v4i b, u2 sb, v4i a, u2 sa, v16f c) {
+__device__ __forceinline__ v16f mfma(v4i b, uint32_t sb, v4i a, uint32_t sa, v16f c) {
   const v8i A = {a.x, a.y, a.z, a.w, 0, 0, 0, 0}, B = {b.x, b.y, b.z, b.w, 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(B, A, c, kE2M1, kE2M1, 2 * (S & 1),
-                                                         static_cast<int>(S < 2 ? sb.x : sb.y), 2 * (S & 1),
-                                                         static_cast<int>(S < 2 ? sa.x : sa.y));
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(B, A, c, kE2M1, kE2M1, 2 * (S & 1), static_cast<int>(sb),
+                                                         2 * (S & 1), static_cast<int>(sa));
+}
+
+template <int S>
+__device__ __forceinline__ uint32_t step_scales(u2 s) {
+  return S < 2 ? s.x : s.y;
 }
 
 // A row's 8 scale bytes of a chunk, shifted so that the bytes of the lane's
-// blocks (2s + g) stand at bytes 0, 2, 4, 6.
+// blocks 2s + g stand at bytes 0, 2, 4, 6.
 __device__ __forceinline__ u2 chunk_scales(u2 row, int g) {
   u2 s;
   s.x = __builtin_amdgcn_alignbyte(row.y, row.x, g);
@@ -109,70 +113,148 @@ __device__ __forceinline__ void tile_of(uint32_t b, uint32_t tm, uint32_t tn, ui
   *n = __builtin_amdgcn_readfirstlane(at / rows);
 }
 
+// Operands reach LDS in pieces of 1 KiB: eight lanes fetch the 128 bytes of a
+// row's chunk, and LDS holds rows of eight 16-byte slots in the order the lanes
+// fetch. Block b of row i stands in slot b ^ (i / 2) % 8, so that the same
+// block of 16 neighbouring rows lies in 16 different groups of four of the 64
+// banks. (Straight to
+// registers a wave would touch 32 rows, 32 bytes each, per load: every line is
+// then asked for four times, and a token's product took 13.4 us instead of
+// 8.4.)
+constexpr int kRowBytes = kChunk * kMxCodeBytes;  // of a row's codes in a chunk
+constexpr int kPieceRows = 8;
+constexpr int kPiece = kPieceRows * kRowBytes;
+
+__device__ __forceinline__ int fetch_block(int piece, int lane) { return (lane & 7) ^ (4 * (piece & 1) + (lane >> 4)); }
+
+// Where block `block` of row `row` (from the start of a piece) stands.
+__device__ __forceinline__ int slot_of(int row, int block) {
+  return row * kRowBytes + (block ^ (row >> 1 & 7)) * kMxCodeBytes;
+}
+
+__device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const uint8_t*)p));
+}
+
+// Fetch 16 bytes a lane from base + off into LDS at `lds` + 16 * lane. No register is written; the caller waits on vmcnt.
+__device__ __forceinline__ void fetch_to_lds(const uint8_t* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+}
+
+// The same if i < n (uniform). The branch is the asm's own: one that the
+// compiler sees splits the loop around it, and its accumulators are then kept
+// twice.
+__device__ __forceinline__ void fetch_to_lds_if(uint32_t i, uint32_t n, const uint8_t* base, uint32_t off, uint32_t lds) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\ts_cmp_ge_u32 %3, %4\n\ts_cbranch_scc1 .Lzdp_skip%=\n\t"
+      "global_load_lds_dwordx4 %1, %2\n.Lzdp_skip%=:" ::"s"(lds), "v"(off), "s"(base), "s"(i), "s"(n)
+      : "memory", "scc");
+}
+
 // ------------------------------------------------------------------------
 // Few output tiles: a block owns an output tile of 32 FM x 32 FN and its waves
-// split the contraction, chunk by chunk in turn; operands go from global memory
-// straight to registers, and the waves' sums are added through LDS in wave
-// order.
+// take the contraction's chunks in turn, each through an LDS space of its own,
+// so that no wave waits for another; the waves' sums are added through LDS in
+// wave order.
 // ------------------------------------------------------------------------
+
+template <int FM, int FN, int NW>
+struct Split {
+  static constexpr int kSpace = (FM + FN) * kFrag * kRowBytes;  // of a wave
+  static constexpr int kPartRow = kFrag + 4;                    // floats, padded
+  static constexpr int kParts = NW * kFrag * kPartRow * 4;
+  static constexpr int kLds = NW * kSpace > kParts ? NW * kSpace : kParts;
+  static_assert(kLds <= 160 * 1024, "LDS of a CU");
+};
 
 template <int FM, int FN, int NW, int DT>
 __global__ void __launch_bounds__(64 * NW) mx_product_split_kernel(const MxProductArgs P) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  using T = Split<FM, FN, NW>;
+  extern __shared__ __align__(16) uint8_t lds[];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 31, g = lane >> 5;
   uint32_t tm, tn;
   tile_of(blockIdx.x, tiles_of(P.m, kFrag * FM), tiles_of(P.n, kFrag * FN), &tm, &tn);
   const int64_t m0 = static_cast<int64_t>(tm) * kFrag * FM, n0 = static_cast<int64_t>(tn) * kFrag * FN;
-  const v4i *ac[FM], *bc[FN];
+  const int64_t mlast = P.m - 1 - m0, nlast = P.n - 1 - n0;  // rows past the end repeat the last one
+  const uint8_t* const abase = P.a_codes + m0 * P.lda * kMxCodeBytes;
+  const uint8_t* const bbase = P.b_codes + n0 * P.ldb * kMxCodeBytes;
+  constexpr int kPieces = (FM + FN) * kFrag / kPieceRows, kPiecesA = FM * kFrag / kPieceRows;
+  uint32_t off[kPieces];
+#pragma unroll
+  for (int j = 0; j < kPieces; ++j) {
+    const bool is_a = j < kPiecesA;
+    int64_t row = (is_a ? j : j - kPiecesA) * kPieceRows + (lane >> 3);
+    const int64_t last = is_a ? mlast : nlast;
+    row = row < last ? row : last;
+    off[j] = static_cast<uint32_t>((row * (is_a ? P.lda : P.ldb) + fetch_block(j, lane)) * kMxCodeBytes);
+  }
   const uint8_t *as[FM], *bs[FN];
 #pragma unroll
   for (int f = 0; f < FM; ++f) {
-    const int64_t i = m0 + f * kFrag + r;
-    const int64_t row = (i < P.m ? i : P.m - 1) * P.lda;
-    ac[f] = reinterpret_cast<const v4i*>(P.a_codes) + row + g;
-    as[f] = P.a_scales + row;
+    const int64_t i = f * kFrag + r;
+    as[f] = P.a_scales + (m0 + (i < mlast ? i : mlast)) * P.lda;
   }
 #pragma unroll
   for (int f = 0; f < FN; ++f) {
-    const int64_t j = n0 + f * kFrag + r;
-    const int64_t row = (j < P.n ? j : P.n - 1) * P.ldb;
-    bc[f] = reinterpret_cast<const v4i*>(P.b_codes) + row + g;
-    bs[f] = P.b_scales + row;
+    const int64_t j = f * kFrag + r;
+    bs[f] = P.b_scales + (n0 + (j < nlast ? j : nlast)) * P.ldb;
   }
+  uint8_t* const mine = lds + w * T::kSpace;
+  const uint32_t to = lds_address(mine);
   v16f acc[FM][FN] = {};
-  for (int64_t k = static_cast<int64_t>(w) * kChunk; k < P.kb; k += NW * kChunk) {
-    v4i a[FM][kSteps], b[FN][kSteps];
+  const int64_t full = P.kb / kChunk, chunks = (P.kb + kChunk - 1) / kChunk;
+  for (int64_t c = w; c < chunks; c += NW) {
+    const uint8_t* const ab = abase + c * kRowBytes;
+    const uint8_t* const bb = bbase + c * kRowBytes;
+    const int64_t left = P.kb - c * kChunk;
     u2 sa[FM], sb[FN];
-    const int64_t left = P.kb - k;
+    if (c < full) {
 #pragma unroll
-    for (int f = 0; f < FN; ++f) {
+      for (int j = 0; j < kPieces; ++j) {
+        // A's pieces past its last row hold rows that no output needs
+        if (j >= kPiecesA || j * kPieceRows <= mlast) fetch_to_lds(j < kPiecesA ? ab : bb, off[j], to + j * kPiece);
+      }
+    } else {
+      // the last, partial chunk: blocks past the end are zero
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) b[f][s] = 2 * s + g < left ? bc[f][k + 2 * s] : (v4i){};
-      sb[f] = load_scales(bs[f] + k, left);
+      for (int j = 0; j < kPieces; ++j) {
+        v4i x = {};
+        if (fetch_block(j, lane) < left) x = *reinterpret_cast<const v4i*>((j < kPiecesA ? ab : bb) + off[j]);
+        *reinterpret_cast<v4i*>(mine + j * kPiece + lane * 16) = x;
+      }
     }
 #pragma unroll
-    for (int f = 0; f < FM; ++f) {
+    for (int f = 0; f < FN; ++f) sb[f] = load_scales(bs[f] + c * kChunk, left);
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) a[f][s] = 2 * s + g < left ? ac[f][k + 2 * s] : (v4i){};
-      sa[f] = load_scales(as[f] + k, left);
-    }
+    for (int f = 0; f < FM; ++f) sa[f] = load_scales(as[f] + c * kChunk, left);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
     for (int f = 0; f < FN; ++f) sb[f] = chunk_scales(sb[f], g);
 #pragma unroll
     for (int f = 0; f < FM; ++f) sa[f] = chunk_scales(sa[f], g);
+    auto step = [&](auto sc) {
+      constexpr int S = decltype(sc)::value;
+      v4i a[FM], b[FN];
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
+      for (int f = 0; f < FM; ++f) a[f] = *reinterpret_cast<const v4i*>(mine + slot_of(f * kFrag + r, 2 * S + g));
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        acc[i][j] = mfma<0>(b[j][0], sb[j], a[i][0], sa[i], acc[i][j]);
-        acc[i][j] = mfma<1>(b[j][1], sb[j], a[i][1], sa[i], acc[i][j]);
-        acc[i][j] = mfma<2>(b[j][2], sb[j], a[i][2], sa[i], acc[i][j]);
-        acc[i][j] = mfma<3>(b[j][3], sb[j], a[i][3], sa[i], acc[i][j]);
-      }
+      for (int f = 0; f < FN; ++f) b[f] = *reinterpret_cast<const v4i*>(mine + slot_of((FM + f) * kFrag + r, 2 * S + g));
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = mfma<S>(b[j], step_scales<S>(sb[j]), a[i], step_scales<S>(sa[i]), acc[i][j]);
+    };
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
+    step(std::integral_constant<int, 2>{});
+    step(std::integral_constant<int, 3>{});
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read out before the next chunk lands there
   }
-  // Sum over the waves, one 32 x 32 fragment at a time: wave w's in part[w],
-  // row-major with a pad of 4 floats.
-  __shared__ float part[NW][kFrag][kFrag + 4];
+  __syncthreads();
+  // Sum over the waves, one 32 x 32 fragment at a time.
+  float* const part = reinterpret_cast<float*>(lds);
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -181,57 +263,58 @@ __global__ void __launch_bounds__(64 * NW) mx_product_split_kernel(const MxProdu
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const f4 x = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-        *reinterpret_cast<f4*>(&part[w][r][8 * q + 4 * g]) = x;
+        *reinterpret_cast<f4*>(part + (w * kFrag + r) * T::kPartRow + 8 * q + 4 * g) = x;
       }
       __syncthreads();
       const int t = threadIdx.x;
-      if (t < kFrag * kFrag / 8) {
-        const int row = t >> 2, col = (t & 3) * 8;
-        float v[8] = {};
+      const int row = t >> 2, col = (t & 3) * 8;
+      const int64_t om = m0 + i * kFrag + row, on = n0 + j * kFrag + col;
+      if (row < kFrag && om < P.m && on < P.n) {
+        f4 x = {}, y = {};
 #pragma unroll
-        for (int u = 0; u < NW; ++u)
-#pragma unroll
-          for (int q = 0; q < 8; ++q) v[q] += part[u][row][col + q];
-        const int64_t om = m0 + i * kFrag + row, on = n0 + j * kFrag + col;
-        if (om < P.m && on < P.n) store8<DT>(P.out, om * P.ldo + on, P.n - on, v);
+        for (int u = 0; u < NW; ++u) {
+          x += *reinterpret_cast<const f4*>(part + (u * kFrag + row) * T::kPartRow + col);
+          y += *reinterpret_cast<const f4*>(part + (u * kFrag + row) * T::kPartRow + col + 4);
+        }
+        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        store8<DT>(P.out, om * P.ldo + on, P.n - on, v);
       }
     }
 }
 
 // ------------------------------------------------------------------------
 // Many output tiles: WM x WN waves, each with FM x FN fragments, share an
-// output tile through LDS, two stages of one chunk each. Codes go from global
-// memory to LDS without passing registers, 16 bytes a lane: eight lanes fetch
-// a row's 128 bytes of the chunk, lane l of eight its block l ^ (row & 7), and
-// LDS holds row after row of eight 16-byte slots in the order the lanes fetch.
-// The reading lane finds block b of a row in slot b ^ (row & 7), so the eight
-// rows that a read touches at a time lie in different banks.
-// A stage's loads are issued when the stage before the last has been read out,
-// a whole stage's products ahead of their use.
+// output tile through LDS, two stages of one chunk each. A stage's codes are
+// fetched while the stage before is multiplied, the loads between the products.
+//
+// Scales pass through registers, four chunks (a group) of a row at a time, a
+// chunk per lane, a quarter of the rows per stage. A row's 8 bytes
+// per stage alone would ask the L2 for a sector of every row in every stage.
+// The loop holds no branch that the compiler sees (fetch_to_lds_if).
 // ------------------------------------------------------------------------
 
-constexpr int kRowBytes = kChunk * kMxCodeBytes;  // of codes per row and stage
+constexpr int kGroupChunks = 4;
 
 template <int FM, int FN, int WM, int WN>
 struct Tile {
   static constexpr int kM = kFrag * FM * WM, kN = kFrag * FN * WN;
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int kRows = kM + kN;                 // A's rows, then B's
-  static constexpr int kLoads = kRows / 8 / kWaves;     // of 1 KiB, per wave and stage
-  static constexpr int kScaleLoads = (kRows + kThreads - 1) / kThreads;
-  static constexpr int kCodes = kRows * kRowBytes;
-  static constexpr int kStage = kCodes + kRows * kChunk;
+  static constexpr int kLoads = kRows / kPieceRows / kWaves;  // pieces, per wave and stage
+  static constexpr int kTurns = kGroupChunks;           // stages that fetch a group's scales
+  static constexpr int kTurnRows = kRows / kTurns;      // whose scales a stage fetches
+  static constexpr int kPend = kTurnRows * kGroupChunks / kThreads;  // in so many loads a lane
+  static constexpr int kStage = kRows * kRowBytes;      // codes of a stage
+  static constexpr int kPlane = kRows * kChunk;         // scales of a stage
   static constexpr int kOutRow = kFrag * FN + 4;        // floats, padded
   static constexpr int kOut = kWaves * kFrag * kOutRow * 4;
-  static constexpr int kLds = 2 * kStage > kOut ? 2 * kStage : kOut;
+  static constexpr int kIn = 2 * kStage + 2 * kGroupChunks * kPlane;
+  static constexpr int kLds = kIn > kOut ? kIn : kOut;
   static_assert(kLds <= 160 * 1024, "LDS of a CU");
-  static_assert(kRows % (8 * kWaves) == 0 && kRows % kThreads == 0, "rows per wave and thread");
+  static_assert(kM % (kPieceRows * kWaves) == 0 && kN % (kPieceRows * kWaves) == 0, "a load's rows belong to one operand");
+  static_assert(kM % kTurnRows == 0 && kN % kTurnRows == 0, "a turn's rows belong to one operand");
+  static_assert(kWaves % 2 == 0, "the pieces of a wave have one parity, so one block per lane");
 };
-
-// Fetch 16 bytes a lane from base + off into LDS at `lds` + 16 * lane. No register is written; the caller waits on vmcnt.
-__device__ __forceinline__ void fetch_to_lds(const uint8_t* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
-}
 
 template <int FM, int FN, int WM, int WN, int DT>
 __global__ void __launch_bounds__(64 * WM * WN, 1) mx_product_tile_kernel(const MxProductArgs P) {
@@ -248,11 +331,11 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_product_tile_kernel(const 
   // where a lane's loads start: row of the tile, block of the chunk
   const uint8_t* const abase = P.a_codes + m0 * P.lda * kMxCodeBytes;
   const uint8_t* const bbase = P.b_codes + n0 * P.ldb * kMxCodeBytes;
-  const int lb = (lane & 7) ^ (lane >> 3);
+  const int lb = fetch_block(w, lane);
   uint32_t off[T::kLoads];
 #pragma unroll
   for (int j = 0; j < T::kLoads; ++j) {
-    int64_t row = (j * T::kWaves + w) * 8 + (lane >> 3);
+    int64_t row = (j * T::kWaves + w) * kPieceRows + (lane >> 3);
     int64_t ld = P.lda;
     if (row >= T::kM) {
       row -= T::kM;
@@ -263,55 +346,93 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_product_tile_kernel(const 
     }
     off[j] = static_cast<uint32_t>((row * ld + lb) * kMxCodeBytes);
   }
-  const uint8_t* srow[T::kScaleLoads];
+  const uint8_t* const sabase = P.a_scales + m0 * P.lda;
+  const uint8_t* const sbbase = P.b_scales + n0 * P.ldb;
+  uint32_t soff[T::kTurns][T::kPend];
 #pragma unroll
-  for (int j = 0; j < T::kScaleLoads; ++j) {
-    int64_t row = j * T::kThreads + threadIdx.x;
-    if (row >= T::kM) {
-      row -= T::kM;
-      srow[j] = P.b_scales + (n0 + (row < nlast ? row : nlast)) * P.ldb;
-    } else {
-      srow[j] = P.a_scales + (m0 + (row < mlast ? row : mlast)) * P.lda;
+  for (int j = 0; j < T::kTurns; ++j)
+#pragma unroll
+    for (int p = 0; p < T::kPend; ++p) {
+      int64_t row = j * T::kTurnRows + p * (T::kTurnRows / T::kPend) + threadIdx.x / kGroupChunks;
+      if (row >= T::kM) {
+        row -= T::kM;
+        soff[j][p] = static_cast<uint32_t>((row < nlast ? row : nlast) * P.ldb);
+      } else {
+        soff[j][p] = static_cast<uint32_t>((row < mlast ? row : mlast) * P.lda);
+      }
     }
-  }
 
-  // A partial last chunk is stage 0, so that every later stage is whole.
-  const int64_t part = P.kb % kChunk, stages = (P.kb + kChunk - 1) / kChunk;
-  auto chunk_of = [&](int64_t i) { return part ? (i == 0 ? stages - 1 : i - 1) : i; };
-  u2 scales[T::kScaleLoads];
-  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
-  auto fetch_scales = [&](int64_t k, int64_t left) {
+  // A partial last chunk is stage 0, so that every later stage is whole; there
+  // is at least one whole chunk.
+  const uint32_t part = P.kb % kChunk, whole = P.kb / kChunk, stages = whole + (part != 0);
+  const uint32_t first = part ? 1 : 0;  // the stage of chunk 0
+  const uint32_t lds0 = lds_address(lds);
+  uint8_t* const planes = lds + 2 * T::kStage;
+  // Chunk c's scales stand in plane c % 8, the partial chunk's in plane 4 until
+  // the chunk that needs it.
+  constexpr int kPartPlane = kGroupChunks;
+  auto plane = [&](uint32_t c) -> uint8_t* { return planes + c % (2 * kGroupChunks) * T::kPlane; };
+  // Turn `turn` of group q: lane l of four fetches chunk 4 q + l (the last whole
+  // one again where there are fewer; nothing uses that copy).
+  u2 pend[T::kPend];
+  auto fetch_scales = [&](uint32_t q, uint32_t turn) {
+    const uint32_t want = q * kGroupChunks + threadIdx.x % kGroupChunks;
+    const uint32_t at = (want < whole ? want : whole - 1) * kChunk;
+    const uint8_t* base = sabase;
 #pragma unroll
-    for (int j = 0; j < T::kScaleLoads; ++j) scales[j] = load_scales(srow[j] + k * kChunk, left);
+    for (int j = 1; j < T::kTurns; ++j) base = turn == j ? (j * T::kTurnRows < T::kM ? sabase : sbbase) : base;
+#pragma unroll
+    for (int p = 0; p < T::kPend; ++p) {
+      uint32_t row = soff[0][p];
+#pragma unroll
+      for (int j = 1; j < T::kTurns; ++j) row = turn == j ? soff[j][p] : row;
+      __builtin_memcpy(&pend[p], base + (row + at), kChunk);
+    }
   };
-  auto fetch = [&](int64_t i, int64_t k, int j) {  // load j of stage i, chunk k
-    const uint8_t* const from = ((j * T::kWaves) * 8 >= T::kM ? bbase : abase) + k * kRowBytes;
-    fetch_to_lds(from, off[j], lds0 + static_cast<uint32_t>(i & 1) * T::kStage + (j * T::kWaves + w) * 1024);
+  auto store_scales = [&](uint32_t q, uint32_t turn) {
+    uint8_t* const to = plane(q * kGroupChunks) + threadIdx.x % kGroupChunks * T::kPlane +
+                        (turn * T::kTurnRows + threadIdx.x / kGroupChunks) * kChunk;
+#pragma unroll
+    for (int p = 0; p < T::kPend; ++p) *reinterpret_cast<u2*>(to + p * (T::kTurnRows / T::kPend) * kChunk) = pend[p];
   };
-  auto publish = [&](int64_t i) {  // the fetched stage, to every wave
+  auto fetch = [&](uint32_t i, int j) {  // load j of stage i (a whole chunk), if there is that stage
+    const uint32_t c = i - first;
+    const uint8_t* const from = (j * T::kWaves * kPieceRows >= T::kM ? bbase : abase) + static_cast<uint64_t>(c) * kRowBytes;
+    fetch_to_lds_if(i, stages, from, off[j], lds0 + (i & 1) * T::kStage + (j * T::kWaves + w) * kPiece);
+  };
+  // The fetched stage i (a whole chunk c), to every wave, with the scales that
+  // the stage before asked for: turn (c - 1) % kTurns of the group after chunk
+  // c - 1's. Then the next turn is asked for.
+  auto publish = [&](uint32_t i) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    uint8_t* const at = lds + (i & 1) * T::kStage + T::kCodes;
-#pragma unroll
-    for (int j = 0; j < T::kScaleLoads; ++j)
-      *reinterpret_cast<u2*>(at + (j * T::kThreads + threadIdx.x) * kChunk) = scales[j];
+    const uint32_t c = i - first, before = c + kGroupChunks - 1;
+    store_scales(before / kGroupChunks, before % T::kTurns);
     __syncthreads();
+    fetch_scales(c / kGroupChunks + 1, c % T::kTurns);
   };
 
   const int wm = w / WN, wn = w % WN;
   const int arow = wm * FM * kFrag + r, brow = T::kM + wn * FN * kFrag + r;
   v4i a[2][FM], b[2][FN];
+  u2 ra[FM], rb[FN];  // a stage's scales as they stand in LDS
   u2 sa[FM], sb[FN];
-  auto read_scales = [&](int64_t i) {
-    const uint8_t* const at = lds + (i & 1) * T::kStage + T::kCodes;
+  auto read_scales = [&](const uint8_t* at) {
 #pragma unroll
-    for (int f = 0; f < FM; ++f) sa[f] = chunk_scales(*reinterpret_cast<const u2*>(at + (arow + f * kFrag) * kChunk), g);
+    for (int f = 0; f < FM; ++f) ra[f] = *reinterpret_cast<const u2*>(at + (arow + f * kFrag) * kChunk);
 #pragma unroll
-    for (int f = 0; f < FN; ++f) sb[f] = chunk_scales(*reinterpret_cast<const u2*>(at + (brow + f * kFrag) * kChunk), g);
+    for (int f = 0; f < FN; ++f) rb[f] = *reinterpret_cast<const u2*>(at + (brow + f * kFrag) * kChunk);
+  };
+  auto own_scales = [&]() {
+#pragma unroll
+    for (int f = 0; f < FM; ++f) sa[f] = chunk_scales(ra[f], g);
+#pragma unroll
+    for (int f = 0; f < FN; ++f) sb[f] = chunk_scales(rb[f], g);
   };
   // Fragment f of step s of stage i: B's first two, A's first, then the rest,
   // in the order in which the products need them.
-  auto read = [&](int64_t i, int s, int f) {
-    const uint8_t* const at = lds + (i & 1) * T::kStage + ((2 * s + g) ^ (r & 7)) * kMxCodeBytes;
+  auto read = [&](uint32_t i, int s, int f) {
+    // (a fragment's first row is a multiple of 32, so r alone gives the slot)
+    const uint8_t* const at = lds + (i & 1) * T::kStage + ((2 * s + g) ^ (r >> 1 & 7)) * kMxCodeBytes;
     constexpr int kFirst = 2;
     if (f < kFirst) b[s & 1][f] = *reinterpret_cast<const v4i*>(at + (brow + f * kFrag) * kRowBytes);
     else if (f == kFirst) a[s & 1][0] = *reinterpret_cast<const v4i*>(at + arow * kRowBytes);
@@ -321,35 +442,35 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_product_tile_kernel(const 
 
   v16f acc[FM][FN] = {};
   constexpr int kGroups = FM * FN / 2;  // pairs of products per step
-  constexpr int kReads = (FM + FN + kGroups - 1) / kGroups, kFetches = (T::kLoads + 2 * kGroups - 1) / (2 * kGroups);
-  // One step: per group, a load or two of the next stage (steps 0 and 1), two
-  // products, and a read or two of the next step's fragments. The order is
-  // fixed, so that loads, reads and products leave in turn.
-  auto step = [&](auto sc, auto morec, int64_t i) {
+  constexpr int kReads = (FM + FN + kGroups - 1) / kGroups;            // per group
+  constexpr int kLateReads = (FM + FN + kGroups - 2) / (kGroups - 1);  // per group of step 3 but its first
+  constexpr int kFetches = (T::kLoads + 2 * kGroups) / (2 * kGroups + 1);
+  // One step: per group two products and a few reads of the next step's
+  // fragments, the order fixed so that reads and products leave in turn. Step 3
+  // publishes the next stage behind its first group (every wave has read this
+  // stage out by then) and starts fetching the one after it into this stage's
+  // place; the next stage's first steps fetch the rest. Behind the last stage
+  // the same happens without fetches, to no effect.
+  auto step = [&](auto sc, uint32_t i) {
     constexpr int S = decltype(sc)::value;
-    constexpr bool more = decltype(morec)::value;  // there is a next stage
-    const int64_t k = more && S < 2 ? chunk_of(i + 1) : 0;
-    u2 ta[FM], tb[FN];
+    // the scales of this step, kept while the next stage's are read
+    uint32_t ta[FM], tb[FN];
 #pragma unroll
-    for (int f = 0; f < FM; ++f) ta[f] = sa[f];
+    for (int f = 0; f < FM; ++f) ta[f] = step_scales<S>(sa[f]);
 #pragma unroll
-    for (int f = 0; f < FN; ++f) tb[f] = sb[f];
-    if constexpr (more && S == 0) fetch_scales(k, kChunk);
+    for (int f = 0; f < FN; ++f) tb[f] = step_scales<S>(sb[f]);
 #pragma unroll
     for (int t = 0; t < kGroups; ++t) {
-      if constexpr (more && S < 2) {
-#pragma unroll
-        for (int q = 0; q < kFetches; ++q) {
-          const int j = (S * kGroups + t) * kFetches + q;
-          if (j < T::kLoads) fetch(i + 1, k, j);
-        }
-      }
-      if constexpr (more && S == 3) {
+      if constexpr (S == 3) {
         if (t == 1) {
           publish(i + 1);
-          read_scales(i + 1);
+          read_scales(plane(i + 1 - first));
         }
       }
+      const int slot = S == 3 ? t - 1 : kGroups - 1 + S * kGroups + t;
+#pragma unroll
+      for (int q = 0; q < kFetches; ++q)
+        if (slot >= 0 && slot * kFetches + q < T::kLoads) fetch(i + (S == 3 ? 2 : 1), slot * kFetches + q);
       const int x = 2 * t / FN, y = 2 * t % FN;
       acc[x][y] = mfma<S>(b[S & 1][y], tb[y], a[S & 1][x], ta[x], acc[x][y]);
       acc[x][y + 1] = mfma<S>(b[S & 1][y + 1], tb[y + 1], a[S & 1][x], ta[x], acc[x][y + 1]);
@@ -357,50 +478,62 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_product_tile_kernel(const 
 #pragma unroll
         for (int q = 0; q < kReads; ++q)
           if (t * kReads + q < FM + FN) read(i, S + 1, t * kReads + q);
-      } else if constexpr (more) {
-        // the reads of the next stage follow its publication
-        constexpr int kLate = (FM + FN + kGroups - 2) / (kGroups - 1);
+      } else {
         if (t > 0) {
 #pragma unroll
-          for (int q = 0; q < kLate; ++q)
-            if ((t - 1) * kLate + q < FM + FN) read(i + 1, 0, (t - 1) * kLate + q);
+          for (int q = 0; q < kLateReads; ++q)
+            if ((t - 1) * kLateReads + q < FM + FN) read(i + 1, 0, (t - 1) * kLateReads + q);
         }
+        if (t == kGroups - 1) own_scales();
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  auto stage = [&](auto morec, int64_t i) {
-    step(std::integral_constant<int, 0>{}, morec, i);
-    step(std::integral_constant<int, 1>{}, morec, i);
-    step(std::integral_constant<int, 2>{}, morec, i);
-    step(std::integral_constant<int, 3>{}, morec, i);
-  };
 
-  if (stages > 0) {
-    if (part) {
-      // blocks past the end are zero
-      const int64_t k = stages - 1;
+  // group 0's scales; the last turn's are left for the first whole stage
 #pragma unroll
-      for (int j = 0; j < T::kLoads; ++j) {
-        v4i x = {};
-        if (lb < part)
-          x = *reinterpret_cast<const v4i*>(((j * T::kWaves) * 8 >= T::kM ? bbase : abase) + k * kRowBytes + off[j]);
-        *reinterpret_cast<v4i*>(lds + (j * T::kWaves + w) * 1024 + lane * 16) = x;
-      }
-      fetch_scales(k, part);
-    } else {
-#pragma unroll
-      for (int j = 0; j < T::kLoads; ++j) fetch(0, 0, j);
-      fetch_scales(0, kChunk);
-    }
-    publish(0);
-    read_scales(0);
-#pragma unroll
-    for (int f = 0; f < FM + FN; ++f) read(0, 0, f);
-    for (int64_t i = 0; i + 1 < stages; ++i) stage(std::true_type{}, i);
-    stage(std::false_type{}, stages - 1);
-    __syncthreads();
+  for (int j = 0; j < kGroupChunks; ++j) {
+    fetch_scales(0, j % T::kTurns);
+    if (j < kGroupChunks - 1) store_scales(0, j % T::kTurns);
   }
+  if (part) {
+    // blocks past the end are zero
+#pragma unroll
+    for (int j = 0; j < T::kLoads; ++j) {
+      v4i x = {};
+      if (lb < static_cast<int>(part))
+        x = *reinterpret_cast<const v4i*>((j * T::kWaves * kPieceRows >= T::kM ? bbase : abase) +
+                                          static_cast<uint64_t>(whole) * kRowBytes + off[j]);
+      *reinterpret_cast<v4i*>(lds + (j * T::kWaves + w) * kPiece + lane * 16) = x;
+    }
+    for (int row = threadIdx.x; row < T::kRows; row += T::kThreads) {
+      const bool of_b = row >= T::kM;
+      const int64_t i = of_b ? row - T::kM : row, last = of_b ? nlast : mlast;
+      const uint8_t* const from = (of_b ? sbbase : sabase) + (i < last ? i : last) * (of_b ? P.ldb : P.lda);
+      *reinterpret_cast<u2*>(plane(kPartPlane) + row * kChunk) =
+          load_scales(from + static_cast<uint64_t>(whole) * kChunk, part);
+    }
+    __syncthreads();
+  } else {
+#pragma unroll
+    for (int j = 0; j < T::kLoads; ++j) fetch(0, j);
+    publish(0);
+  }
+  read_scales(part ? plane(kPartPlane) : plane(0));
+  own_scales();
+#pragma unroll
+  for (int f = 0; f < FM + FN; ++f) read(0, 0, f);
+  // what step 3 of the stage before would have fetched
+#pragma unroll
+  for (int j = 0; j < (kGroups - 1) * kFetches && j < T::kLoads; ++j) fetch(1, j);
+  uint32_t i = 0;
+  do {
+    step(std::integral_constant<int, 0>{}, i);
+    step(std::integral_constant<int, 1>{}, i);
+    step(std::integral_constant<int, 2>{}, i);
+    step(std::integral_constant<int, 3>{}, i);
+  } while (++i < stages);
+  __syncthreads();
 
   // 32 rows of the wave's part of the tile at a time, through LDS, so that a
   // row leaves in runs of 8 columns a lane.
@@ -429,51 +562,58 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_product_tile_kernel(const 
   }
 }
 
-template <int FM, int FN, int NW, int DT>
-hipError_t split_launch(const MxProductArgs& a, hipStream_t s) {
-  const int64_t tiles = mx_tiles(a.m, kFrag * FM) * mx_tiles(a.n, kFrag * FN);
-  hipLaunchKernelGGL((mx_product_split_kernel<FM, FN, NW, DT>), dim3(static_cast<uint32_t>(tiles)), dim3(64 * NW), 0, s,
-                     a);
-  return hipGetLastError();
-}
-
-template <int FM, int FN, int WM, int WN, int DT>
-hipError_t tile_launch(const MxProductArgs& a, hipStream_t s) {
-  using T = Tile<FM, FN, WM, WN>;
-  const auto kernel = mx_product_tile_kernel<FM, FN, WM, WN, DT>;
-  // more than the default limit of 64 KiB of dynamic LDS, granted once per device
-  static std::atomic<uint64_t> granted{0};
+// Launch with more than the default limit of 64 KiB of dynamic LDS, granted once per kernel and device.
+template <typename Kernel>
+hipError_t launch_with_lds(Kernel kernel, int64_t tiles, int threads, int lds, std::atomic<uint64_t>& granted,
+                           const MxProductArgs& a, hipStream_t s) {
   int dev = 0;
   if (hipError_t e = hipGetDevice(&dev)) return e;
   const uint64_t bit = uint64_t{1} << (dev & 63);
   if (dev > 63 || !(granted.load(std::memory_order_acquire) & bit)) {
     if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds))
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, lds))
       return e;
     granted.fetch_or(bit, std::memory_order_release);
   }
-  const int64_t tiles = mx_tiles(a.m, T::kM) * mx_tiles(a.n, T::kN);
-  hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(tiles)), dim3(T::kThreads), T::kLds, s, a);
+  hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(tiles)), dim3(threads), lds, s, a);
   return hipGetLastError();
 }
 
-enum Variant { kSplit32, kSplit64x32, kSplit64, kTile256 };
-
-Variant pick(const MxProductArgs& a) {
-  if (mx_tiles(a.m, 256) * mx_tiles(a.n, 256) >= 128) return kTile256;
-  if (a.m > 64 && a.n > 64) return kSplit64;
-  return a.m > 32 ? kSplit64x32 : kSplit32;
+template <int FM, int FN, int NW, int DT>
+hipError_t split_launch(const MxProductArgs& a, hipStream_t s) {
+  static std::atomic<uint64_t> granted{0};
+  return launch_with_lds(mx_product_split_kernel<FM, FN, NW, DT>, mx_tiles(a.m, kFrag * FM) * mx_tiles(a.n, kFrag * FN),
+                         64 * NW, Split<FM, FN, NW>::kLds, granted, a, s);
 }
+
+template <int FM, int FN, int WM, int WN, int DT>
+hipError_t tile_launch(const MxProductArgs& a, hipStream_t s) {
+  using T = Tile<FM, FN, WM, WN>;
+  static std::atomic<uint64_t> granted{0};
+  return launch_with_lds(mx_product_tile_kernel<FM, FN, WM, WN, DT>, mx_tiles(a.m, T::kM) * mx_tiles(a.n, T::kN),
+                         T::kThreads, T::kLds, granted, a, s);
+}
+
+// The largest tile of which there are enough to keep the 256 CUs busy, and for
+// a few tiles the waves of a block split the contraction. Measured (us, K =
+// 4096, the variant taken and its neighbour): 4096 x 3100, 208 tiles of 256^2:
+// 40 against 50 (128^2); 4096 x 2048, 128 tiles: 30 (128^2) against 34; 1000 x
+// 4096, 256 tiles of 128^2: 20 against 26 (64^2); 700 x 2500, 120 tiles: 15
+// (64^2) against 18; 300 x 2000, 160 tiles of 64^2: 9.7 against 10.1 (32^2);
+// 100 x 4096, 128 tiles: 7.3 (32^2) against 9.8. The tiles' loop needs a whole
+// chunk. Eight waves a block leave room for two blocks on a CU, four for four:
+// 1 x 14336, 448 tiles of 32^2: 7.8 with four waves against 8.4 with eight;
+// 1 x 4096 at K = 14336, 128 tiles: 8.8 with eight against 13.1 with four.
+constexpr int64_t kEnoughTiles = 160;
+constexpr int64_t kCus = 256;
 
 template <int DT>
 hipError_t product_launch(const MxProductArgs& a, hipStream_t s) {
-  switch (pick(a)) {
-    case kSplit32: return split_launch<1, 1, 8, DT>(a, s);
-    case kSplit64x32: return split_launch<2, 1, 8, DT>(a, s);
-    case kSplit64: return split_launch<2, 2, 4, DT>(a, s);
-    case kTile256: return tile_launch<4, 2, 2, 4, DT>(a, s);
-  }
-  return hipErrorInvalidValue;
+  auto tiles = [&](int64_t side) { return mx_tiles(a.m, side) * mx_tiles(a.n, side); };
+  if (a.kb >= kChunk && tiles(256) >= kEnoughTiles) return tile_launch<4, 2, 2, 4, DT>(a, s);
+  if (a.kb >= kChunk && tiles(128) >= kEnoughTiles) return tile_launch<2, 2, 2, 2, DT>(a, s);
+  if (tiles(64) >= kEnoughTiles) return split_launch<2, 2, 4, DT>(a, s);
+  return tiles(32) > kCus ? split_launch<1, 1, 4, DT>(a, s) : split_launch<1, 1, 8, DT>(a, s);
 }
 
 }  // namespace
