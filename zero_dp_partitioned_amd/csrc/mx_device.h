@@ -32,16 +32,59 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
 // The conversions take the scale as an fp32 whose exponent field is the byte.
 __device__ __forceinline__ float scale_operand(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-// Eight values divided by the block's scale and rounded to E2M1 codes (nearest
-// even, saturating at +-6), element 0 in the low nibble. A NaN block's codes
-// are 0.
-__device__ __forceinline__ uint32_t encode8(const float v[8], uint32_t byte) {
+// Eight values in their own type DT (ZERO_DT_F32 / F16 / BF16), as they lie in memory.
+template <int DT>
+struct Raw8 {
+  static constexpr int kWords = DT == ZERO_DT_F32 ? 8 : 4;
+  uint32_t w[kWords];
+};
+
+// The bits, in fp32, of the largest magnitude. 16-bit magnitudes compare as
+// their bits too, two at a time.
+template <int DT>
+__device__ __forceinline__ uint32_t max_bits(const uint32_t* w, int words) {
+  uint32_t m = 0;
+  if constexpr (DT == ZERO_DT_F32) {
+#pragma unroll
+    for (int q = 0; q < words; ++q) {
+      const uint32_t b = w[q] & 0x7FFFFFFFu;
+      m = b > m ? b : m;
+    }
+    return m;
+  } else {
+    typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int q = 0; q < words; ++q)
+      m = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2, m),
+                                                                 __builtin_bit_cast(us2, w[q] & 0x7FFF7FFFu)));
+    const uint32_t top = (m >> 16) > (m & 0xFFFFu) ? m >> 16 : m & 0xFFFFu;
+    return __float_as_uint(decode16<DT == ZERO_DT_BF16 ? kSrcBF16 : kSrcF16>(top));
+  }
+}
+
+// Two values (fp32 words lo and hi, or the two halves of one 16-bit word `lo`)
+// divided by the scale s and rounded to E2M1 codes (nearest even, saturating at
+// +-6), into byte SEL of c.
+template <int DT, int SEL>
+__device__ __forceinline__ uint32_t encode2(uint32_t c, uint32_t lo, uint32_t hi, float s) {
+  if constexpr (DT == ZERO_DT_F32)
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(lo), __uint_as_float(hi), s, SEL);
+  else if constexpr (DT == ZERO_DT_BF16)
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf2, lo), s, SEL);
+  else
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(h2, lo), s, SEL);
+}
+
+// Eight values' codes, element 0 in the low nibble. A NaN block's are 0.
+template <int DT>
+__device__ __forceinline__ uint32_t encode8(const uint32_t* w, uint32_t byte) {
+  constexpr int K = DT == ZERO_DT_F32 ? 2 : 1;  // words per pair
   const float s = scale_operand(byte);
   uint32_t c = 0;
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0], v[1], s, 0);
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], s, 1);
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], s, 2);
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], s, 3);
+  c = encode2<DT, 0>(c, w[0], w[K - 1], s);
+  c = encode2<DT, 1>(c, w[K], w[2 * K - 1], s);
+  c = encode2<DT, 2>(c, w[2 * K], w[3 * K - 1], s);
+  c = encode2<DT, 3>(c, w[3 * K], w[4 * K - 1], s);
   return byte == 255u ? 0u : c;
 }
 

@@ -610,9 +610,10 @@ constexpr int64_t kCus = 256;
 template <int DT>
 hipError_t product_launch(const MxProductArgs& a, hipStream_t s) {
   auto tiles = [&](int64_t side) { return mx_tiles(a.m, side) * mx_tiles(a.n, side); };
-  if (a.kb >= kChunk && tiles(256) >= kEnoughTiles) return tile_launch<4, 2, 2, 4, DT>(a, s);
-  if (a.kb >= kChunk && tiles(128) >= kEnoughTiles) return tile_launch<2, 2, 2, 2, DT>(a, s);
-  if (tiles(64) >= kEnoughTiles) return split_launch<2, 2, 4, DT>(a, s);
+  const int64_t side = a.m < a.n ? a.m : a.n;  // a tile has more than half its rows and columns to do
+  if (a.kb >= kChunk && side > 128 && tiles(256) >= kEnoughTiles) return tile_launch<4, 2, 2, 4, DT>(a, s);
+  if (a.kb >= kChunk && side > 64 && tiles(128) >= kEnoughTiles) return tile_launch<2, 2, 2, 2, DT>(a, s);
+  if (side > 32 && tiles(64) >= kEnoughTiles) return split_launch<2, 2, 4, DT>(a, s);
   return tiles(32) > kCus ? split_launch<1, 1, 4, DT>(a, s) : split_launch<1, 1, 8, DT>(a, s);
 }
 

@@ -14,78 +14,68 @@ constexpr int kLane = 8;                   // values a lane handles
 constexpr int kMxGroups = 4;               // groups of 8 a lane has in flight
 constexpr int kLanesPerBlock = kMxBlock / kLane;
 
-// Values e .. e+7 of a row of which `left` values from e on exist; the missing
-// ones are 0. DT: ZERO_DT_F32 / F16 / BF16, any alignment of the type.
+// The eight values at p, at any alignment of the type, of which `left` exist; the missing ones are 0.
 template <int DT>
-__device__ __forceinline__ void load8(const void* row, int64_t e, int64_t left, float v[8]) {
-  if constexpr (DT == ZERO_DT_F32) {
-    const float* p = static_cast<const float*>(row) + e;
-    if (left >= 8) {
-      f4 a, b;
-      __builtin_memcpy(&a, p, 16);
-      __builtin_memcpy(&b, p + 4, 16);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
+__device__ __forceinline__ Raw8<DT> load8(const void* p, int64_t left) {
+  Raw8<DT> x = {};
+  if (left >= 8) {
+    __builtin_memcpy(x.w, p, sizeof x.w);
+  } else if constexpr (DT == ZERO_DT_F32) {
+    const uint32_t* f = static_cast<const uint32_t*>(p);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = q < left ? p[q] : 0.0f;
-    }
+    for (int q = 0; q < 8; ++q)
+      if (q < left) x.w[q] = f[q];
   } else {
-    constexpr int K = DT == ZERO_DT_BF16 ? kSrcBF16 : kSrcF16;
-    const uint16_t* p = static_cast<const uint16_t*>(row) + e;
-    if (left >= 8) {
-      u4 a;
-      __builtin_memcpy(&a, p, 16);
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    const uint16_t* h = static_cast<const uint16_t*>(p);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        v[2 * q] = decode16<K>(w[q] & 0xFFFFu);
-        v[2 * q + 1] = decode16<K>(w[q] >> 16);
-      }
-    } else {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = q < left ? decode16<K>(p[q]) : 0.0f;
-    }
+    for (int q = 0; q < 8; ++q)
+      if (q < left) x.w[q / 2] |= static_cast<uint32_t>(h[q]) << (16 * (q & 1));
   }
-}
-
-__device__ __forceinline__ uint32_t max_bits8(const float v[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const uint32_t b = __float_as_uint(v[q]) & 0x7FFFFFFFu;
-    m = b > m ? b : m;
-  }
-  return m;
+  return x;
 }
 
 // ------------------------------------------------------------------------
 // Quantise along the rows. Item i is quarter i % 4 of block i / 4, blocks
-// counted row by row.
+// counted row by row. FLAT: one row (a shard, or a dense matrix of whole
+// blocks); a full tile's loads are then all in flight before the first is used,
+// which takes 117M fp32 values from FLAT_BEFORE to FLAT_AFTER us.
 // ------------------------------------------------------------------------
 
-template <int DT>
+template <int DT, bool FLAT>
 __global__ void __launch_bounds__(kBlock) mx_quantize_rows_kernel(const MxQuantArgs Q) {
+  constexpr int kElem = DT == ZERO_DT_F32 ? 4 : 2;
   const int64_t kb = (Q.cols + kMxBlock - 1) / kMxBlock;
-  const int64_t items = Q.rows * kb * kLanesPerBlock;
+  const int64_t items = (FLAT ? 1 : Q.rows) * kb * kLanesPerBlock;
   constexpr int64_t T = static_cast<int64_t>(kBlock) * kMxGroups;
+  const int lane = threadIdx.x % kLanesPerBlock;
+  const char* const src = static_cast<const char*>(Q.src);
+  auto put = [&](const Raw8<DT>& x, int64_t at, bool there) {
+    const uint32_t byte = scale_byte(quad_max(max_bits<DT>(x.w, Raw8<DT>::kWords)));
+    const uint32_t c = encode8<DT>(x.w, byte);
+    if (there) {
+      st_stream(reinterpret_cast<uint32_t*>(Q.codes) + at * 4 + lane, c);
+      if (lane == 0) Q.scales[at] = static_cast<uint8_t>(byte);
+    }
+  };
   for (int64_t t0 = blockIdx.x * T; t0 < items; t0 += gridDim.x * T) {
+    if (FLAT && (t0 + T) * kLane <= Q.cols) {
+      Raw8<DT> x[kMxGroups];
+#pragma unroll
+      for (int k = 0; k < kMxGroups; ++k) {
+        const char* const p = src + (t0 + k * kBlock + threadIdx.x) * kLane * kElem;
+        __builtin_memcpy(x[k].w, p, sizeof x[k].w);
+      }
+#pragma unroll
+      for (int k = 0; k < kMxGroups; ++k) put(x[k], (t0 + k * kBlock + threadIdx.x) / kLanesPerBlock, true);
+      continue;
+    }
 #pragma unroll
     for (int k = 0; k < kMxGroups; ++k) {
       const int64_t i = t0 + k * kBlock + threadIdx.x;
       const int64_t b = i / kLanesPerBlock;
-      const int64_t row = Q.rows == 1 ? 0 : b / kb, bk = b - row * kb;
-      const int64_t e = bk * kMxBlock + (i % kLanesPerBlock) * kLane;
-      const int elem = DT == ZERO_DT_F32 ? 4 : 2;
-      float v[8];
-      load8<DT>(static_cast<const char*>(Q.src) + row * Q.src_ld * elem, e, i < items ? Q.cols - e : 0, v);
-      const uint32_t byte = scale_byte(quad_max(max_bits8(v)));
-      const uint32_t c = encode8(v, byte);
-      if (i < items) {
-        const int64_t at = row * Q.ld + bk;
-        reinterpret_cast<uint32_t*>(Q.codes)[at * 4 + i % kLanesPerBlock] = c;
-        if (i % kLanesPerBlock == 0) Q.scales[at] = static_cast<uint8_t>(byte);
-      }
+      const int64_t row = FLAT ? 0 : b / kb, bk = b - row * kb;
+      const int64_t e = bk * kMxBlock + lane * kLane;
+      put(load8<DT>(src + (row * Q.src_ld + e) * kElem, i < items ? Q.cols - e : 0), row * Q.ld + bk, i < items);
     }
   }
 }
@@ -124,40 +114,30 @@ __global__ void __launch_bounds__(kBlock) mx_quantize_tile_kernel(const MxQuantA
     const int64_t wide = tc - strip * kStrip < kStrip ? tc - strip * kStrip : kStrip;
     const int64_t r0 = at / wide * kSide, c0 = (strip * kStrip + at % wide) * kSide;
     const int64_t e = c0 + (tid % kSideLanes) * kLane;
-    float v[kPasses][8];
+    const int i0 = tid / kSideLanes;
+    const char* const src = static_cast<const char*>(Q.src) + ((r0 + i0) * Q.src_ld + e) * kElem;
+    const int64_t down = Q.src_ld * kElem * (kBlock / kSideLanes);  // bytes from pass to pass
+    Raw8<DT> v[kPasses];
+    if (r0 + kSide <= Q.rows && c0 + kSide <= Q.cols) {
 #pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
-      const int64_t row = r0 + p * (kBlock / kSideLanes) + tid / kSideLanes;
-      load8<DT>(static_cast<const char*>(Q.src) + row * Q.src_ld * kElem, e, row < Q.rows ? Q.cols - e : 0, v[p]);
+      for (int p = 0; p < kPasses; ++p) __builtin_memcpy(v[p].w, src + p * down, sizeof v[p].w);
+    } else {
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p)
+        v[p] = load8<DT>(src + p * down, r0 + i0 + p * (kBlock / kSideLanes) < Q.rows ? Q.cols - e : 0);
     }
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
-      const int i = p * (kBlock / kSideLanes) + tid / kSideLanes;
+      const int i = p * (kBlock / kSideLanes) + i0;
       uint32_t* const to = tile + i * kDwords;
       const int first = (tid % kSideLanes) * kLane / kPer;
-      if constexpr (DT == ZERO_DT_F32) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const f4 x = {v[p][4 * h], v[p][4 * h + 1], v[p][4 * h + 2], v[p][4 * h + 3]};
-          *reinterpret_cast<f4*>(to + ((first + 4 * h) ^ (i / 32 * 16))) = x;
-        }
-      } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          // the 16-bit patterns again (the conversion to fp32 lost nothing)
-          if constexpr (DT == ZERO_DT_BF16) {
-            w[q] = (__float_as_uint(v[p][2 * q]) >> 16) | (__float_as_uint(v[p][2 * q + 1]) & 0xFFFF0000u);
-          } else {
-            const h2 h = {static_cast<_Float16>(v[p][2 * q]), static_cast<_Float16>(v[p][2 * q + 1])};
-            w[q] = __builtin_bit_cast(uint32_t, h);
-          }
-        }
-        *reinterpret_cast<u4*>(to + (first ^ (i / 32 * 16))) = (u4){w[0], w[1], w[2], w[3]};
-      }
+      for (int h = 0; h < Raw8<DT>::kWords / 4; ++h)
+        *reinterpret_cast<u4*>(to + ((first + 4 * h) ^ (i / 32 * 16))) =
+            (u4){v[p].w[4 * h], v[p].w[4 * h + 1], v[p].w[4 * h + 2], v[p].w[4 * h + 3]};
       if (Q.codes) {
-        const uint32_t byte = scale_byte(quad_max(max_bits8(v[p])));
-        const uint32_t c = encode8(v[p], byte);
+        const uint32_t byte = scale_byte(quad_max(max_bits<DT>(v[p].w, Raw8<DT>::kWords)));
+        const uint32_t c = encode8<DT>(v[p].w, byte);
         if (r0 + i < Q.rows && e / kMxBlock * kMxBlock < Q.cols) {
           const int64_t b = (r0 + i) * Q.ld + e / kMxBlock;
           reinterpret_cast<uint32_t*>(Q.codes)[b * 4 + tid % 4] = c;
@@ -170,29 +150,21 @@ __global__ void __launch_bounds__(kBlock) mx_quantize_tile_kernel(const MxQuantA
 #pragma unroll
     for (int h = 0; h < 2 / kPer; ++h) {
       const int d = h * 64 + tid / 4;  // the dword: kPer columns
-      float x[kPer][kMxBlock];
+      uint32_t w[kMxBlock];
 #pragma unroll
-      for (int q = 0; q < kMxBlock; ++q) {
-        const uint32_t w = tile[(rb * kMxBlock + q) * kDwords + (d ^ (rb * 16))];
-        if constexpr (DT == ZERO_DT_F32) {
-          x[0][q] = __uint_as_float(w);
-        } else {
-          constexpr int K = DT == ZERO_DT_BF16 ? kSrcBF16 : kSrcF16;
-          x[0][q] = decode16<K>(w & 0xFFFFu);
-          x[kPer - 1][q] = decode16<K>(w >> 16);
-        }
-      }
+      for (int q = 0; q < kMxBlock; ++q) w[q] = tile[(rb * kMxBlock + q) * kDwords + (d ^ (rb * 16))];
 #pragma unroll
       for (int y = 0; y < kPer; ++y) {
-        uint32_t m = 0;
+        uint32_t x[4 * Raw8<DT>::kWords];  // the column's 32 values
 #pragma unroll
-        for (int q = 0; q < kMxBlock; q += 8) {
-          const uint32_t n = max_bits8(&x[y][q]);
-          m = n > m ? n : m;
+        for (int q = 0; q < 4 * Raw8<DT>::kWords; ++q) {
+          if constexpr (DT == ZERO_DT_F32) x[q] = w[q];
+          else x[q] = __builtin_amdgcn_perm(w[2 * q + 1], w[2 * q], y ? 0x07060302u : 0x05040100u);
         }
-        const uint32_t byte = scale_byte(m);
-        const u4 c = {encode8(&x[y][0], byte), encode8(&x[y][8], byte), encode8(&x[y][16], byte),
-                      encode8(&x[y][24], byte)};
+        constexpr int K = Raw8<DT>::kWords;
+        const uint32_t byte = scale_byte(max_bits<DT>(x, 4 * K));
+        const u4 c = {encode8<DT>(x, byte), encode8<DT>(x + K, byte), encode8<DT>(x + 2 * K, byte),
+                      encode8<DT>(x + 3 * K, byte)};
         const int64_t col = c0 + d * kPer + y;
         if (col < Q.cols && r0 + rb * kMxBlock < Q.rows) {
           const int64_t b = col * Q.ld_t + r0 / kMxBlock + rb;
@@ -384,7 +356,9 @@ hipError_t quantize_launch(const MxQuantArgs& a, hipStream_t s) {
     q.rows = 1;
   }
   const int64_t items = q.rows * mx_blocks(q.cols) * kLanesPerBlock;
-  hipLaunchKernelGGL((mx_quantize_rows_kernel<DT>), dim3(mx_grid(items, kBlock * kMxGroups)), dim3(kBlock), 0, s, q);
+  const dim3 grid(mx_grid(items, kBlock * kMxGroups));
+  if (q.rows == 1) hipLaunchKernelGGL((mx_quantize_rows_kernel<DT, true>), grid, dim3(kBlock), 0, s, q);
+  else hipLaunchKernelGGL((mx_quantize_rows_kernel<DT, false>), grid, dim3(kBlock), 0, s, q);
   return hipGetLastError();
 }
 
