@@ -33,6 +33,9 @@ __device__ __forceinline__ void st_stream(T* p, T x) {
   __builtin_nontemporal_store(x, p);
 }
 
+// 16 bytes at any alignment of a smaller type.
+typedef u4 u4_any __attribute__((aligned(2)));
+
 // ------------------------------------------------------------------------
 // 16-bit encodings
 // ------------------------------------------------------------------------

@@ -1,6 +1,8 @@
 // Device helpers of the microscaled 4-bit kernels.
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.h"
 #include "mx_internal.h"
 
@@ -11,12 +13,19 @@ typedef float f2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 
-// Lanes of a quad that share a 32-value block: lane l ^ 1 and lane l ^ 2.
-__device__ __forceinline__ uint32_t quad_max(uint32_t x) {
+// The largest of 4 or 8 neighbouring lanes.
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t x) {
+  static_assert(LANES == 4 || LANES == 8, "");
   const uint32_t a = __builtin_amdgcn_update_dpp(0, x, 0xB1, 0xF, 0xF, true);  // lanes 1,0,3,2
   x = x > a ? x : a;
   const uint32_t b = __builtin_amdgcn_update_dpp(0, x, 0x4E, 0xF, 0xF, true);  // lanes 2,3,0,1
-  return x > b ? x : b;
+  x = x > b ? x : b;
+  if constexpr (LANES == 8) {
+    const uint32_t c = __builtin_amdgcn_update_dpp(0, x, 0x141, 0xF, 0xF, true);  // 7,6,5,4,3,2,1,0 of eight
+    x = x > c ? x : c;
+  }
+  return x;
 }
 
 // The scale byte of a block from the bits of its largest magnitude: the
@@ -32,11 +41,14 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
 // The conversions take the scale as an fp32 whose exponent field is the byte.
 __device__ __forceinline__ float scale_operand(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-// Eight values in their own type DT (ZERO_DT_F32 / F16 / BF16), as they lie in memory.
+// 16 bytes of values of type DT (ZERO_DT_F32 / F16 / BF16), as they lie in memory.
 template <int DT>
-struct Raw8 {
-  static constexpr int kWords = DT == ZERO_DT_F32 ? 8 : 4;
-  uint32_t w[kWords];
+struct Raw {
+  static constexpr int kElem = DT == ZERO_DT_F32 ? 4 : 2;
+  static constexpr int kVals = 16 / kElem;
+  static constexpr int kLanes = kMxBlock / kVals;  // that share a block
+  using Codes = typename std::conditional<DT == ZERO_DT_F32, uint16_t, uint32_t>::type;  // of kVals values
+  uint32_t w[4];
 };
 
 // The bits, in fp32, of the largest magnitude. 16-bit magnitudes compare as
@@ -75,27 +87,28 @@ __device__ __forceinline__ uint32_t encode2(uint32_t c, uint32_t lo, uint32_t hi
     return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(h2, lo), s, SEL);
 }
 
-// Eight values' codes, element 0 in the low nibble. A NaN block's are 0.
+// The codes of Raw<DT>::kVals values, element 0 in the low nibble. A NaN block's are 0.
 template <int DT>
-__device__ __forceinline__ uint32_t encode8(const uint32_t* w, uint32_t byte) {
-  constexpr int K = DT == ZERO_DT_F32 ? 2 : 1;  // words per pair
+__device__ __forceinline__ uint32_t encode(const uint32_t* w, uint32_t byte) {
   const float s = scale_operand(byte);
   uint32_t c = 0;
-  c = encode2<DT, 0>(c, w[0], w[K - 1], s);
-  c = encode2<DT, 1>(c, w[K], w[2 * K - 1], s);
-  c = encode2<DT, 2>(c, w[2 * K], w[3 * K - 1], s);
-  c = encode2<DT, 3>(c, w[3 * K], w[4 * K - 1], s);
+  if constexpr (DT == ZERO_DT_F32) {
+    c = encode2<DT, 0>(c, w[0], w[1], s);
+    c = encode2<DT, 1>(c, w[2], w[3], s);
+  } else {
+    c = encode2<DT, 0>(c, w[0], 0, s);
+    c = encode2<DT, 1>(c, w[1], 0, s);
+    c = encode2<DT, 2>(c, w[2], 0, s);
+    c = encode2<DT, 3>(c, w[3], 0, s);
+  }
   return byte == 255u ? 0u : c;
 }
 
-// Eight codes times the block's scale, in fp32 (exact; NaN for a NaN block).
-__device__ __forceinline__ void decode8(uint32_t c, float s, float v[8]) {
+// Four codes (the low 16 bits of c) times the scale s, in fp32 (exact; NaN for the scale of a NaN block).
+__device__ __forceinline__ f4 decode4(uint32_t c, float s) {
   const f2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0);
   const f2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1);
-  const f2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2);
-  const f2 e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3);
-  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
-  v[4] = d.x; v[5] = d.y; v[6] = e.x; v[7] = e.y;
+  return (f4){a.x, a.y, b.x, b.y};
 }
 
 }  // namespace
