@@ -28,6 +28,23 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t x) {
   return x;
 }
 
+// Four lanes' a[0..3], transposed: lane l's a[k] becomes lane k's a[l].
+__device__ __forceinline__ void quad_transpose(uint32_t a[4], int lane) {
+  const bool odd = lane & 1, high = lane & 2;
+#pragma unroll
+  for (int k = 0; k < 4; k += 2) {
+    const uint32_t t = __builtin_amdgcn_update_dpp(0, odd ? a[k] : a[k + 1], 0xB1, 0xF, 0xF, true);
+    a[k] = odd ? t : a[k];
+    a[k + 1] = odd ? a[k + 1] : t;
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t t = __builtin_amdgcn_update_dpp(0, high ? a[k] : a[k + 2], 0x4E, 0xF, 0xF, true);
+    a[k] = high ? t : a[k];
+    a[k + 2] = high ? a[k + 2] : t;
+  }
+}
+
 // The scale byte of a block from the bits of its largest magnitude: the
 // exponent field of max |v| less 2 (E2M1's largest exponent), at least 0; a
 // zero or subnormal maximum has field 0 and gets 0 as well. Infinity and NaN

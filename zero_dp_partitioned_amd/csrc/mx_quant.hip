@@ -5,7 +5,7 @@
 // time (4 fp32 or 8 16-bit values), next to its neighbours' 16 bytes, with the
 // non-temporal hint: the lines are then whole in one access and leave the
 // caches to the narrow side. (With 8 fp32 values a lane, two accesses to every
-// other 16 bytes, widening 117M values to fp32 took 136 us instead of WIDEN32;
+// other 16 bytes, widening 117M values to fp32 took 136 us instead of 75;
 // plain stores cost the 16-bit side 55 us instead of 43.) Eight or four lanes
 // share a block; its maximum is two or three lane permutes.
 #include "mx_device.h"
@@ -119,7 +119,12 @@ __global__ void __launch_bounds__(kBlock) mx_quantize_rows_kernel(const MxQuantA
 // ------------------------------------------------------------------------
 
 constexpr int kSide = 128;                     // values of a tile, either way
-constexpr int kStrip = 4;                      // tiles next to each other that are worked on in turn
+// Every XCD works along strips of kStrip tile rows, column by column: the halves
+// of a line of codes are then written soon after one another by the same L2,
+// and the tiles in flight cover all channels. (Neighbouring tiles on different
+// XCDs, in strips of columns: an XCD's tiles lay in few channels, and 8192 x
+// 14336 took 99 us instead of 87.)
+constexpr int kStrip = 4;
 
 template <int DT>
 __global__ void __launch_bounds__(kBlock) mx_quantize_tile_kernel(const MxQuantArgs Q) {
@@ -133,12 +138,50 @@ __global__ void __launch_bounds__(kBlock) mx_quantize_tile_kernel(const MxQuantA
   const int64_t tr = (Q.rows + kSide - 1) / kSide, tc = (Q.cols + kSide - 1) / kSide;
   const int64_t tiles = tr * tc;
   const int tid = threadIdx.x;
+  // The rows' blocks of a lane's kPasses rows (i0, i0 + kStep, ...) of the tile at r0, value column e.
+  auto rows_out = [&](const R* v, int64_t r0, int i0, int64_t e) {
+    uint32_t c[kPasses], byte[kPasses];
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      byte[p] = scale_byte(lanes_max<R::kLanes>(max_bits<DT>(v[p].w, 4)));
+      c[p] = encode<DT>(v[p].w, byte[p]);
+    }
+    const bool there = e / kMxBlock * kMxBlock < Q.cols;
+    if constexpr (R::kLanes == 4) {
+      // the four lanes of a block take one of four rows' blocks each: whole
+      // blocks and a fourth of the stores
+      const int l = tid % 4;
+#pragma unroll
+      for (int p = 0; p < kPasses; p += 4) {
+        quad_transpose(c + p, l);
+        const uint32_t mine = l & 2 ? (l & 1 ? byte[p + 3] : byte[p + 2]) : (l & 1 ? byte[p + 1] : byte[p]);
+        const int64_t row = r0 + i0 + (p + l) * kStep;
+        if (there && row < Q.rows) {
+          const int64_t b = row * Q.ld + e / kMxBlock;
+          *reinterpret_cast<u4*>(Q.codes + b * kMxCodeBytes) = (u4){c[p], c[p + 1], c[p + 2], c[p + 3]};
+          Q.scales[b] = static_cast<uint8_t>(mine);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const int64_t row = r0 + i0 + p * kStep;
+        if (there && row < Q.rows) {
+          const int64_t b = row * Q.ld + e / kMxBlock;
+          reinterpret_cast<typename R::Codes*>(Q.codes)[b * R::kLanes + tid % R::kLanes] =
+              static_cast<typename R::Codes>(c[p]);
+          if (tid % R::kLanes == 0) Q.scales[b] = static_cast<uint8_t>(byte[p]);
+        }
+      }
+    }
+  };
   for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-    // strips of kStrip tile columns, row by row: the halves of a line of codes
-    // and the pieces of a line of scales are written soon after one another
-    const int64_t strip = t / (tr * kStrip), at = t - strip * tr * kStrip;
-    const int64_t wide = tc - strip * kStrip < kStrip ? tc - strip * kStrip : kStrip;
-    const int64_t r0 = at / wide * kSide, c0 = (strip * kStrip + at % wide) * kSide;
+    // block t runs on XCD t % 8: a run of tiles for every XCD
+    const int64_t each = tiles / 8, more = tiles % 8, x = t % 8;
+    const int64_t i = x * each + (x < more ? x : more) + t / 8;
+    const int64_t strip = i / (tc * kStrip), at = i - strip * tc * kStrip;
+    const int64_t high = tr - strip * kStrip < kStrip ? tr - strip * kStrip : kStrip;
+    const int64_t r0 = (strip * kStrip + at % high) * kSide, c0 = at / high * kSide;
     const int x0 = tid % kSideLanes * R::kVals, i0 = tid / kSideLanes;
     const int64_t e = c0 + x0;
     const char* const src = static_cast<const char*>(Q.src) + ((r0 + i0) * Q.src_ld + e) * R::kElem;
@@ -157,17 +200,8 @@ __global__ void __launch_bounds__(kBlock) mx_quantize_tile_kernel(const MxQuantA
       const int i = p * kStep + i0;
       *reinterpret_cast<u4*>(tile + i * kDwords + (x0 / kPer ^ (i / 32 * 16))) =
           (u4){v[p].w[0], v[p].w[1], v[p].w[2], v[p].w[3]};
-      if (Q.codes) {
-        const uint32_t byte = scale_byte(lanes_max<R::kLanes>(max_bits<DT>(v[p].w, 4)));
-        const uint32_t c = encode<DT>(v[p].w, byte);
-        if (r0 + i < Q.rows && e / kMxBlock * kMxBlock < Q.cols) {
-          const int64_t b = (r0 + i) * Q.ld + e / kMxBlock;
-          reinterpret_cast<typename R::Codes*>(Q.codes)[b * R::kLanes + tid % R::kLanes] =
-              static_cast<typename R::Codes>(c);
-          if (tid % R::kLanes == 0) Q.scales[b] = static_cast<uint8_t>(byte);
-        }
-      }
     }
+    if (Q.codes) rows_out(v, r0, i0, e);
     __syncthreads();
     const int rb = tid % 4;  // the column's block of 32
 #pragma unroll
