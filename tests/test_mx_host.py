@@ -122,7 +122,6 @@ def test_product_refusals(lib):
         assert call(**kw) == zdp.ERR_ALIGNMENT, kw
     assert call(m=2 ** 31) == zdp.ERR_UNSUPPORTED
     assert call(n=2 ** 31, ldo=2 ** 31) == zdp.ERR_UNSUPPORTED
-    assert call(m=2 ** 31 - 1, n=2 ** 31 - 1, ldo=2 ** 31 - 1) in (zdp.ERR_UNSUPPORTED, zdp.ERR_INVALID_ARG)
     assert call(lda=2 ** 20) == zdp.ERR_UNSUPPORTED
     assert call(ldb=2 ** 20) == zdp.ERR_UNSUPPORTED
     assert call(m=0, a=None, sa=None, out=None) == zdp.OK

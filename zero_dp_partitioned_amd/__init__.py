@@ -715,8 +715,12 @@ def mx_reduce_grad_segment(codes, scales, avg_out, workspace, group, state, stre
     n_d = len(codes)
     if not n_d or n_d != len(scales):
         raise ValueError(f"{n_d} copies of codes and {len(scales)} of scales")
-    for r in range(n_d):
-        _need_flat(codes[r], scales[r], f"copy {r}", dev, 0, n)
+    u8, kb = _torch().uint8, -(-n // MX_BLOCK)
+    for r, (c, s) in enumerate(zip(codes, scales)):
+        if not (type(c) is type(s) is type(avg_out) and c.dtype == s.dtype == u8 and c.get_device() == dev
+                and s.get_device() == dev and c.is_contiguous() and s.is_contiguous() and s.numel() >= kb
+                and c.numel() >= 16 * kb):
+            _need_flat(c, s, f"copy {r}", dev, 0, n)  # says what is wrong, if anything
     _call(load().zero_mx_reduce_grad_segment, dev, stream, _ptr_array(codes), _ptr_array(scales), n_d, n,
           avg_out.data_ptr(), workspace.data_ptr(), _nbytes(workspace), group, state.data_ptr())
 

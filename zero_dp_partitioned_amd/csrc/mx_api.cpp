@@ -178,7 +178,6 @@ int zero_mx_product(const void* a_codes, const void* a_scales, int64_t lda, cons
   if (m == 0 || n == 0) return ZERO_OK;
   if (lda > kMxMaxLd || ldb > kMxMaxLd)
     return fail(ZERO_ERR_UNSUPPORTED, "rows more than %lld blocks apart", (long long)kMxMaxLd);
-  if ((m + 31) / 32 * ((n + 31) / 32) > INT32_MAX) return fail(ZERO_ERR_UNSUPPORTED, "too many output tiles");
   if (int rc = check_device()) return rc;
   MxProductArgs P;
   P.a_codes = static_cast<const uint8_t*>(a_codes);
@@ -193,6 +192,7 @@ int zero_mx_product(const void* a_codes, const void* a_scales, int64_t lda, cons
   P.out = out;
   P.ldo = ldo;
   hipError_t e = launch_mx_product(P, out_dt, static_cast<hipStream_t>(stream));
+  if (e == hipErrorInvalidConfiguration) return fail(ZERO_ERR_UNSUPPORTED, "more output tiles than a launch holds");
   return e == hipSuccess ? ZERO_OK : hip_fail(e, "product launch");
 }
 

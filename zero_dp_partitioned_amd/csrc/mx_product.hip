@@ -64,32 +64,47 @@ __device__ __forceinline__ u2 load_scales(const uint8_t* p, int64_t left) {
   return s;
 }
 
-// Columns [col, col + 8) of an output row, as far as they exist.
+// A run of kRun = 16 bytes' worth of columns of an output row from column `at` on,
+// as far as they exist. WHOLE: every row starts at a multiple of 16 bytes, so
+// that lanes side by side write whole lines; those go past the caches (8192 x
+// 14336 x 4096 in bf16: 280 -> 258 us; with rows off alignment, where lines are
+// shared between two accesses, the hint cost 98 us instead of 80 at 1001 x
+// 50257 x 1600).
 template <int DT>
-__device__ __forceinline__ void store8(void* out, int64_t at, int64_t left, const float v[8]) {
+struct Run {
+  static constexpr int kElem = DT == ZERO_DT_F32 ? 4 : 2;
+  static constexpr int kCols = 16 / kElem;
+};
+
+__device__ __forceinline__ bool whole_lines(const void* out, int64_t ldo, int elem) {
+  return ((reinterpret_cast<uintptr_t>(out) | static_cast<uintptr_t>(ldo * elem)) & 15) == 0;
+}
+
+template <int DT, bool WHOLE>
+__device__ __forceinline__ void store_run(void* out, int64_t at, int64_t left, const float* v) {
+  u4 x;
   if constexpr (DT == ZERO_DT_F32) {
-    float* p = static_cast<float*>(out) + at;
-    if (left >= 8) {
-      const f4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
-      __builtin_memcpy(p, &a, 16);
-      __builtin_memcpy(p + 4, &b, 16);
-    } else {
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (q < left) p[q] = v[q];
-    }
+    x = (u4){__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
   } else {
-    uint16_t* p = static_cast<uint16_t*>(out) + at;
     uint32_t h[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) h[q] = encode16(v[q], DT);
-    if (left >= 8) {
-      const u4 w = {h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
-      __builtin_memcpy(p, &w, 16);
+    x = (u4){h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
+  }
+  char* const p = static_cast<char*>(out) + at * Run<DT>::kElem;
+  if (left >= Run<DT>::kCols) {
+    if constexpr (WHOLE) st_stream(reinterpret_cast<u4*>(p), x);
+    else __builtin_memcpy(p, &x, 16);
+  } else {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    if constexpr (DT == ZERO_DT_F32) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (q < left) reinterpret_cast<uint32_t*>(p)[q] = w[q];
     } else {
 #pragma unroll
       for (int q = 0; q < 8; ++q)
-        if (q < left) p[q] = static_cast<uint16_t>(h[q]);
+        if (q < left) reinterpret_cast<uint16_t*>(p)[q] = static_cast<uint16_t>(w[q / 2] >> (16 * (q & 1)));
     }
   }
 }
@@ -266,18 +281,22 @@ __global__ void __launch_bounds__(64 * NW) mx_product_split_kernel(const MxProdu
         *reinterpret_cast<f4*>(part + (w * kFrag + r) * T::kPartRow + 8 * q + 4 * g) = x;
       }
       __syncthreads();
-      const int t = threadIdx.x;
-      const int row = t >> 2, col = (t & 3) * 8;
+      constexpr int kCols = Run<DT>::kCols, kRuns = kFrag / kCols;  // of a row
+      static_assert(kFrag * kRuns <= 64 * NW, "a run per thread");
+      const int row = threadIdx.x / kRuns, col = threadIdx.x % kRuns * kCols;
       const int64_t om = m0 + i * kFrag + row, on = n0 + j * kFrag + col;
       if (row < kFrag && om < P.m && on < P.n) {
-        f4 x = {}, y = {};
+        f4 x[kCols / 4] = {};
 #pragma unroll
-        for (int u = 0; u < NW; ++u) {
-          x += *reinterpret_cast<const f4*>(part + (u * kFrag + row) * T::kPartRow + col);
-          y += *reinterpret_cast<const f4*>(part + (u * kFrag + row) * T::kPartRow + col + 4);
-        }
-        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        store8<DT>(P.out, om * P.ldo + on, P.n - on, v);
+        for (int u = 0; u < NW; ++u)
+#pragma unroll
+          for (int q = 0; q < kCols / 4; ++q)
+            x[q] += *reinterpret_cast<const f4*>(part + (u * kFrag + row) * T::kPartRow + col + 4 * q);
+        float v[kCols];
+#pragma unroll
+        for (int q = 0; q < kCols; ++q) v[q] = x[q / 4][q % 4];
+        if (whole_lines(P.out, P.ldo, Run<DT>::kElem)) store_run<DT, true>(P.out, om * P.ldo + on, P.n - on, v);
+        else store_run<DT, false>(P.out, om * P.ldo + on, P.n - on, v);
       }
     }
 }
@@ -536,36 +555,47 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_product_tile_kernel(const 
   __syncthreads();
 
   // 32 rows of the wave's part of the tile at a time, through LDS, so that a
-  // row leaves in runs of 8 columns a lane.
+  // row leaves in runs of 16 bytes a lane.
   float* const mine = reinterpret_cast<float*>(lds) + w * kFrag * T::kOutRow;
+  auto write = [&](auto whole) {
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
+    for (int i = 0; i < FM; ++i) {
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
+      for (int j = 0; j < FN; ++j)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const f4 x = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-        *reinterpret_cast<f4*>(mine + r * T::kOutRow + j * kFrag + 8 * q + 4 * g) = x;
+        for (int q = 0; q < 4; ++q) {
+          const f4 x = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+          *reinterpret_cast<f4*>(mine + r * T::kOutRow + j * kFrag + 8 * q + 4 * g) = x;
+        }
+      __builtin_amdgcn_wave_barrier();
+      constexpr int kCols = Run<DT>::kCols, kRuns = kFrag * FN / kCols;  // of a row
+#pragma unroll
+      for (int t = 0; t < kFrag * kRuns / 64; ++t) {
+        const int row = (t * 64 + lane) / kRuns, col = (t * 64 + lane) % kRuns * kCols;
+        float v[kCols];
+#pragma unroll
+        for (int q = 0; q < kCols / 4; ++q) {
+          const f4 x = *reinterpret_cast<const f4*>(mine + row * T::kOutRow + col + 4 * q);
+          v[4 * q] = x.x;
+          v[4 * q + 1] = x.y;
+          v[4 * q + 2] = x.z;
+          v[4 * q + 3] = x.w;
+        }
+        const int64_t om = m0 + (wm * FM + i) * kFrag + row, on = n0 + wn * FN * kFrag + col;
+        if (om < P.m && on < P.n) store_run<DT, decltype(whole)::value>(P.out, om * P.ldo + on, P.n - on, v);
       }
-    __builtin_amdgcn_wave_barrier();
-    constexpr int kRuns = kFrag * FN / 8;  // of a row
-#pragma unroll
-    for (int t = 0; t < kFrag * kRuns / 64; ++t) {
-      const int row = (t * 64 + lane) / kRuns, col = (t * 64 + lane) % kRuns * 8;
-      const f4 x = *reinterpret_cast<const f4*>(mine + row * T::kOutRow + col);
-      const f4 y = *reinterpret_cast<const f4*>(mine + row * T::kOutRow + col + 4);
-      const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-      const int64_t om = m0 + (wm * FM + i) * kFrag + row, on = n0 + wn * FN * kFrag + col;
-      if (om < P.m && on < P.n) store8<DT>(P.out, om * P.ldo + on, P.n - on, v);
+      __builtin_amdgcn_wave_barrier();
     }
-    __builtin_amdgcn_wave_barrier();
-  }
+  };
+  if (whole_lines(P.out, P.ldo, Run<DT>::kElem)) write(std::true_type{});
+  else write(std::false_type{});
 }
 
 // Launch with more than the default limit of 64 KiB of dynamic LDS, granted once per kernel and device.
 template <typename Kernel>
 hipError_t launch_with_lds(Kernel kernel, int64_t tiles, int threads, int lds, std::atomic<uint64_t>& granted,
                            const MxProductArgs& a, hipStream_t s) {
+  if (tiles > UINT32_MAX / threads) return hipErrorInvalidConfiguration;  // a launch counts its threads in 32 bits
   int dev = 0;
   if (hipError_t e = hipGetDevice(&dev)) return e;
   const uint64_t bit = uint64_t{1} << (dev & 63);

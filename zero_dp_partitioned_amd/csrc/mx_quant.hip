@@ -19,7 +19,7 @@ constexpr int kMxGroups = 4;  // of 16 bytes a lane has in flight
 template <int DT>
 __device__ __forceinline__ Raw<DT> load16(const void* p) {
   Raw<DT> x;
-  const u4 y = ld_stream(static_cast<const u4_any*>(p));
+  const u4_any y = __builtin_nontemporal_load(static_cast<const u4_any*>(p));
   __builtin_memcpy(x.w, &y, sizeof x.w);
   return x;
 }
@@ -48,7 +48,7 @@ __device__ __forceinline__ Raw<DT> load16(const void* p, int64_t left) {
 template <int DT>
 __device__ __forceinline__ void store16(void* p, u4 x, int64_t left) {
   if (left >= Raw<DT>::kVals) {
-    st_stream(static_cast<u4_any*>(p), x);
+    __builtin_nontemporal_store(static_cast<u4_any>(x), static_cast<u4_any*>(p));
   } else {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     if constexpr (DT == ZERO_DT_F32) {
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kBlock) mx_widen_kernel(const MxWidenArgs W) {
       }
 #pragma unroll
       for (int k = 0; k < kMxGroups; ++k)
-        st_stream(reinterpret_cast<u4_any*>(out + (t0 + k * kBlock + threadIdx.x) * 16), widen<DT>(c[k], byte[k]));
+        store16<DT>(out + (t0 + k * kBlock + threadIdx.x) * 16, widen<DT>(c[k], byte[k]), R::kVals);
       continue;
     }
 #pragma unroll
