@@ -551,54 +551,72 @@ def mx_view(codes, scales, offset, rows, cols):
     return (codes[16 * b:16 * (b + n)].view(rows, cols // 2), scales[b:b + n].view(rows, cols // MX_BLOCK))
 
 
-_MX_DT = {}
+class _MxTypes:
+    """What the 4-bit calls look up on every call, found once (torch is imported on first use)."""
+
+    def __init__(self):
+        torch = _torch()
+        self.tensor = torch.Tensor
+        self.u8, self.f32 = torch.uint8, torch.float32
+        self.values = {torch.float32: DT_F32, torch.float16: DT_F16, torch.bfloat16: DT_BF16}
+        self.stream = torch._C._cuda_getCurrentRawStream
+        self.device = torch._C._cuda_getDevice
+        self.on = torch.cuda.device
+
+
+_MX_TYPES = None
+
+
+def _mx():
+    global _MX_TYPES
+    if _MX_TYPES is None:
+        _MX_TYPES = _MxTypes()
+    return _MX_TYPES
 
 
 def _mx_types():
-    """Value dtypes of the 4-bit calls and their codes (torch is imported on first use)."""
-    if not _MX_DT:
-        torch = _torch()
-        _MX_DT.update({torch.float32: DT_F32, torch.float16: DT_F16, torch.bfloat16: DT_BF16})
-    return _MX_DT
-
-
-def _u8():
-    return (_torch().uint8,)
+    return _mx().values
 
 
 def _device_of(t, name):
     """The index of the device a tensor is on."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _mx().tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     return t.get_device()
 
 
 def _call(fn, device, stream, *args):
     """Call an entry point on `device`'s current stream (or the one given), with that device current."""
-    torch = _torch()
-    s = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
-    if torch._C._cuda_getDevice() == device:
+    mx = _mx()
+    s = mx.stream(device) if stream is None else stream.cuda_stream
+    if mx.device() == device:
         rc = fn(*args, s)
     else:
-        with torch.cuda.device(device):
+        with mx.on(device):
             rc = fn(*args, s)
     if rc != OK:
         raise ZeroError(rc, last_error())
 
 
-def _need_rows(t, name, dtypes, device):
-    """(rows, cols, elements from row to row) of a 2-D tensor of one of `dtypes` on `device` (an index, -1 for the
-    host) with dense rows."""
-    if not isinstance(t, _torch().Tensor):
+def _refuse(t, name, dtypes, device):
+    """Say what keeps `t` from being a tensor of one of `dtypes` on `device` (an index, -1 for the host)."""
+    if not isinstance(t, _mx().tensor):
         raise TypeError(f"{name}: a torch tensor is expected, got {type(t).__name__}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
     if t.get_device() != device:
         raise ValueError(f"{name}: tensor on {t.device}, expected device {device}")
-    if t.dim() != 2:
-        raise ValueError(f"{name}: {t.dim()} dimensions, expected 2")
-    rows, cols = t.shape
+
+
+def _need_rows(t, name, dtypes, device):
+    """(rows, cols, elements from row to row) of a 2-D tensor of one of `dtypes` on `device` (an index, -1 for the
+    host) with dense rows."""
+    if not isinstance(t, _mx().tensor) or t.dtype not in dtypes or t.get_device() != device:
+        _refuse(t, name, dtypes, device)
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: {len(shape)} dimensions, expected 2")
+    rows, cols = shape
     s0, s1 = t.stride()
     if s1 != 1 and cols > 1:
         raise ValueError(f"{name}: its rows are not dense")
@@ -611,7 +629,7 @@ def _need_rows(t, name, dtypes, device):
 
 def _need_mx(codes, scales, name, device, rows=None, values=None):
     """(rows, blocks a row, blocks from row to row) of a 4-bit matrix (2-D codes and scales)."""
-    u8 = _u8()
+    u8 = (_mx().u8,)
     rc, cc, ld_c = _need_rows(codes, name, u8, device)
     r, kb, ld = _need_rows(scales, name, u8, device)
     if rc != r or cc != 16 * kb:
@@ -627,12 +645,8 @@ def _need_mx(codes, scales, name, device, rows=None, values=None):
 
 def _need_values(t, name, dtypes, device):
     """The length of a dense tensor of one of `dtypes` on `device` (an index)."""
-    if not isinstance(t, _torch().Tensor):
-        raise TypeError(f"{name}: a torch tensor is expected, got {type(t).__name__}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
-    if t.get_device() != device:
-        raise ValueError(f"{name}: tensor on {t.device}, expected device {device}")
+    if not isinstance(t, _mx().tensor) or t.dtype not in dtypes or t.get_device() != device:
+        _refuse(t, name, dtypes, device)
     if not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous")
     return t.numel()
@@ -641,7 +655,7 @@ def _need_values(t, name, dtypes, device):
 def _need_flat(codes, scales, name, device, offset, n):
     """The last block (exclusive) of elements [offset, offset + n) of a flat 4-bit vector that holds them, and its
     blocks."""
-    u8 = _u8()
+    u8 = (_mx().u8,)
     nbytes = _need_values(codes, name, u8, device)
     blocks = _need_values(scales, name, u8, device)
     if offset < 0 or offset % MX_BLOCK:
@@ -657,7 +671,7 @@ def mx_cast_writeback(master, codes, scales, offset=0, stream=None):
     of 32). A shard that ends inside a block must end the vector: the block's
     other values would belong to the next rank."""
     dev = _device_of(master, "master")
-    n = _need_values(master, "master", _f32(), dev)
+    n = _need_values(master, "master", (_mx().f32,), dev)
     end, blocks = _need_flat(codes, scales, "flat vector", dev, offset, n)
     if n % MX_BLOCK and end != blocks:
         raise ValueError(f"a shard of {n} values ends inside a block that is not the vector's last one")
@@ -711,11 +725,11 @@ def mx_reduce_grad_segment(codes, scales, avg_out, workspace, group, state, stre
     """reduce_grad_segment over copies in 4 bits: codes and scales are lists of
     N_d flat vectors (1-D uint8), each holding the segment from element 0."""
     dev = _state_device(state, workspace).index
-    n = _need_values(avg_out, "avg_out", _f32(), dev)
+    n = _need_values(avg_out, "avg_out", (_mx().f32,), dev)
     n_d = len(codes)
     if not n_d or n_d != len(scales):
         raise ValueError(f"{n_d} copies of codes and {len(scales)} of scales")
-    u8, kb = _torch().uint8, -(-n // MX_BLOCK)
+    u8, kb = _mx().u8, -(-n // MX_BLOCK)
     for r, (c, s) in enumerate(zip(codes, scales)):
         if not (type(c) is type(s) is type(avg_out) and c.dtype == s.dtype == u8 and c.get_device() == dev
                 and s.get_device() == dev and c.is_contiguous() and s.is_contiguous() and s.numel() >= kb

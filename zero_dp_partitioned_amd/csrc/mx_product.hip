@@ -21,7 +21,6 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 
 constexpr int kE2M1 = 4;     // the instruction's format code for both operands
 constexpr int kChunk = 8;    // blocks of the contraction per chunk
-constexpr int kSteps = 4;    // instructions per chunk and output tile of 32 x 32
 constexpr int kFrag = 32;    // rows of an operand per instruction
 
 // Step s of a chunk multiplies blocks 2s and 2s + 1. `sa` and `sb` hold the
@@ -394,7 +393,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_product_tile_kernel(const 
   // Turn `turn` of group q: lane l of four fetches chunk 4 q + l (the last whole
   // one again where there are fewer; nothing uses that copy).
   u2 pend[T::kPend];
-  auto fetch_scales = [&](uint32_t q, uint32_t turn) {
+  auto fetch_scales = [&](uint32_t q, uint32_t turn, u2* to) {
     const uint32_t want = q * kGroupChunks + threadIdx.x % kGroupChunks;
     const uint32_t at = (want < whole ? want : whole - 1) * kChunk;
     const uint8_t* base = sabase;
@@ -405,14 +404,14 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_product_tile_kernel(const 
       uint32_t row = soff[0][p];
 #pragma unroll
       for (int j = 1; j < T::kTurns; ++j) row = turn == j ? soff[j][p] : row;
-      __builtin_memcpy(&pend[p], base + (row + at), kChunk);
+      __builtin_memcpy(&to[p], base + (row + at), kChunk);
     }
   };
-  auto store_scales = [&](uint32_t q, uint32_t turn) {
+  auto store_scales = [&](uint32_t q, uint32_t turn, const u2* from) {
     uint8_t* const to = plane(q * kGroupChunks) + threadIdx.x % kGroupChunks * T::kPlane +
                         (turn * T::kTurnRows + threadIdx.x / kGroupChunks) * kChunk;
 #pragma unroll
-    for (int p = 0; p < T::kPend; ++p) *reinterpret_cast<u2*>(to + p * (T::kTurnRows / T::kPend) * kChunk) = pend[p];
+    for (int p = 0; p < T::kPend; ++p) *reinterpret_cast<u2*>(to + p * (T::kTurnRows / T::kPend) * kChunk) = from[p];
   };
   auto fetch = [&](uint32_t i, int j) {  // load j of stage i (a whole chunk), if there is that stage
     const uint32_t c = i - first;
@@ -425,9 +424,9 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_product_tile_kernel(const 
   auto publish = [&](uint32_t i) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     const uint32_t c = i - first, before = c + kGroupChunks - 1;
-    store_scales(before / kGroupChunks, before % T::kTurns);
+    store_scales(before / kGroupChunks, before % T::kTurns, pend);
     __syncthreads();
-    fetch_scales(c / kGroupChunks + 1, c % T::kTurns);
+    fetch_scales(c / kGroupChunks + 1, c % T::kTurns, pend);
   };
 
   const int wm = w / WN, wn = w % WN;
@@ -509,12 +508,20 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_product_tile_kernel(const 
     }
   };
 
-  // group 0's scales; the last turn's are left for the first whole stage
+  // The first stage's codes (unless it is the partial chunk) and group 0's
+  // scales, all in flight at once; the last turn's are left for the first whole
+  // stage.
+  if (!part) {
 #pragma unroll
-  for (int j = 0; j < kGroupChunks; ++j) {
-    fetch_scales(0, j % T::kTurns);
-    if (j < kGroupChunks - 1) store_scales(0, j % T::kTurns);
+    for (int j = 0; j < T::kLoads; ++j) fetch(0, j);
   }
+  u2 group[T::kTurns][T::kPend];
+#pragma unroll
+  for (int j = 0; j < T::kTurns; ++j) fetch_scales(0, j, group[j]);
+#pragma unroll
+  for (int j = 0; j < T::kTurns - 1; ++j) store_scales(0, j, group[j]);
+#pragma unroll
+  for (int p = 0; p < T::kPend; ++p) pend[p] = group[T::kTurns - 1][p];
   if (part) {
     // blocks past the end are zero
 #pragma unroll
@@ -534,8 +541,6 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_product_tile_kernel(const 
     }
     __syncthreads();
   } else {
-#pragma unroll
-    for (int j = 0; j < T::kLoads; ++j) fetch(0, j);
     publish(0);
   }
   read_scales(part ? plane(kPartPlane) : plane(0));
