@@ -508,14 +508,36 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_product_tile_kernel(const 
     }
   };
 
-  // The first stage's codes (unless it is the partial chunk) and group 0's
-  // scales, all in flight at once; the last turn's are left for the first whole
-  // stage.
-  if (!part) {
+  // The first stage's codes (the partial chunk's through registers, blocks past
+  // the end zero) and group 0's scales, all in flight at once; the last turn's
+  // are left for the first whole stage. Of the second stage what step 3 of the
+  // stage before would have fetched.
+  constexpr int kEarly = (kGroups - 1) * kFetches < T::kLoads ? (kGroups - 1) * kFetches : T::kLoads;
+  constexpr int kOwnRows = (T::kRows + T::kThreads - 1) / T::kThreads;
+  v4i part_codes[T::kLoads];
+  u2 part_scales[kOwnRows], group[T::kTurns][T::kPend];
+  if (part) {
+#pragma unroll
+    for (int j = 0; j < T::kLoads; ++j) {
+      part_codes[j] = (v4i){};
+      if (lb < static_cast<int>(part))
+        part_codes[j] = *reinterpret_cast<const v4i*>((j * T::kWaves * kPieceRows >= T::kM ? bbase : abase) +
+                                                      static_cast<uint64_t>(whole) * kRowBytes + off[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kOwnRows; ++j) {
+      const int row = j * T::kThreads + threadIdx.x < T::kRows ? j * T::kThreads + threadIdx.x : T::kRows - 1;
+      const bool of_b = row >= T::kM;
+      const int64_t i = of_b ? row - T::kM : row, last = of_b ? nlast : mlast;
+      const uint8_t* const from = (of_b ? sbbase : sabase) + (i < last ? i : last) * (of_b ? P.ldb : P.lda);
+      part_scales[j] = load_scales(from + static_cast<uint64_t>(whole) * kChunk, part);
+    }
+#pragma unroll
+    for (int j = 0; j < kEarly; ++j) fetch(1, j);
+  } else {
 #pragma unroll
     for (int j = 0; j < T::kLoads; ++j) fetch(0, j);
   }
-  u2 group[T::kTurns][T::kPend];
 #pragma unroll
   for (int j = 0; j < T::kTurns; ++j) fetch_scales(0, j, group[j]);
 #pragma unroll
@@ -523,21 +545,13 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_product_tile_kernel(const 
 #pragma unroll
   for (int p = 0; p < T::kPend; ++p) pend[p] = group[T::kTurns - 1][p];
   if (part) {
-    // blocks past the end are zero
 #pragma unroll
-    for (int j = 0; j < T::kLoads; ++j) {
-      v4i x = {};
-      if (lb < static_cast<int>(part))
-        x = *reinterpret_cast<const v4i*>((j * T::kWaves * kPieceRows >= T::kM ? bbase : abase) +
-                                          static_cast<uint64_t>(whole) * kRowBytes + off[j]);
-      *reinterpret_cast<v4i*>(lds + (j * T::kWaves + w) * kPiece + lane * 16) = x;
-    }
-    for (int row = threadIdx.x; row < T::kRows; row += T::kThreads) {
-      const bool of_b = row >= T::kM;
-      const int64_t i = of_b ? row - T::kM : row, last = of_b ? nlast : mlast;
-      const uint8_t* const from = (of_b ? sbbase : sabase) + (i < last ? i : last) * (of_b ? P.ldb : P.lda);
-      *reinterpret_cast<u2*>(plane(kPartPlane) + row * kChunk) =
-          load_scales(from + static_cast<uint64_t>(whole) * kChunk, part);
+    for (int j = 0; j < T::kLoads; ++j)
+      *reinterpret_cast<v4i*>(lds + (j * T::kWaves + w) * kPiece + lane * 16) = part_codes[j];
+#pragma unroll
+    for (int j = 0; j < kOwnRows; ++j) {
+      const int row = j * T::kThreads + threadIdx.x;
+      if (row < T::kRows) *reinterpret_cast<u2*>(plane(kPartPlane) + row * kChunk) = part_scales[j];
     }
     __syncthreads();
   } else {
@@ -547,9 +561,10 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_product_tile_kernel(const 
   own_scales();
 #pragma unroll
   for (int f = 0; f < FM + FN; ++f) read(0, 0, f);
-  // what step 3 of the stage before would have fetched
+  if (!part) {
 #pragma unroll
-  for (int j = 0; j < (kGroups - 1) * kFetches && j < T::kLoads; ++j) fetch(1, j);
+    for (int j = 0; j < kEarly; ++j) fetch(1, j);
+  }
   uint32_t i = 0;
   do {
     step(std::integral_constant<int, 0>{}, i);
