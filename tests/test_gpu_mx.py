@@ -376,6 +376,78 @@ def test_product_strided(m, n, kb, extra, dt):
     assert (buf[:, 0] == 5.0).all() and (buf[:, n + 1:] == 5.0).all()
 
 
+def _check_large(out, a, b, dt):
+    """_check_product's bound with the 64-bit products on the device."""
+    a64, b64 = (torch.from_numpy(_mx.decode(*t)).to(DEV) for t in (a, b))
+    ref, size = a64 @ b64.t(), a64.abs() @ b64.abs().t()
+    got, nan = out.double(), torch.isnan(ref)
+    assert torch.equal(torch.isnan(got), nan)
+    got, ref, size = got[~nan], ref[~nan], size[~nan]
+    bound = a64.shape[1] * 2.0 ** -23 * size
+    bound = bound + HALF_STEP[dt] * (ref.abs() + bound) + TINY[dt]
+    err = (got - ref).abs()
+    assert torch.isfinite(got).all() and (err <= bound).all(), f"worst {float((err / bound).max())} of the bound"
+    if dt == "f32":
+        assert float(err.norm()) <= 1e-6 * float(size.norm())
+
+
+# Whole and partial chunks of 8 blocks, whole and partial groups of 4 chunks, on both sides of each.
+TILE_BLOCKS = [8, 9, 15, 16, 23, 24, 31, 32, 33, 40, 41, 50, 63, 64, 65, 71, 100]
+
+
+@pytest.mark.parametrize("kb", TILE_BLOCKS)
+@pytest.mark.parametrize("m, n", [(1700, 1600), (1665, 1603), (3300, 3328), (3311, 3331)])
+def test_product_of_many_tiles(m, n, kb):
+    """Enough output for the tiles of 128 and 256, ragged and whole, rows of outputs on and off 16 bytes; operands
+    dense and inside wider arrays at odd strides."""
+    g = np.random.default_rng(m + kb)
+    dt = list(DTS)[(kb + m) % 3]
+    extra = (kb * 7 + n) % 4
+    a, b = _mx.random_mx(g, m, kb + extra, 118, 126), _mx.random_mx(g, n, kb + extra, 118, 126)
+    a[1][:, kb:] = 255
+    b[1][:, kb:] = 255
+    a[1][m // 3, kb - 1] = 255  # one row of NaN
+    args = [_up(t) for t in (*a, *b)]
+    args = [t[:, :kb * (16 if q % 2 == 0 else 1)] for q, t in enumerate(args)]
+    out = torch.full((m, n), 9.0, dtype=DTS[dt], device=DEV)
+    zdp.mx_product(*args, out)
+    cut = tuple((c[:, :16 * kb], s[:, :kb]) for c, s in (a, b))
+    _check_large(out, *cut, dt)
+    again = torch.empty_like(out)
+    zdp.mx_product(*args, again)
+    assert torch.equal(out.view(torch.int32 if dt == "f32" else torch.int16),
+                       again.view(torch.int32 if dt == "f32" else torch.int16)), "another run gave other bits"
+
+
+@pytest.mark.parametrize("m, n", [(1700, 1600), (3300, 3331)])
+def test_product_of_many_tiles_inside_a_wider_output(m, n):
+    g = np.random.default_rng(n)
+    a, b = _mx.random_mx(g, m, 18, 118, 126), _mx.random_mx(g, n, 18, 118, 126)
+    for dt in DTS:
+        buf = torch.full((m, n + 5), 5.0, dtype=DTS[dt], device=DEV)
+        out = buf[:, 3:n + 3]
+        zdp.mx_product(*(_up(t) for t in (*a, *b)), out)
+        _check_large(out, a, b, dt)
+        assert (buf[:, :3] == 5.0).all() and (buf[:, n + 3:] == 5.0).all()
+
+
+def test_captured_without_a_call_before():
+    """The first call of a kernel with more LDS than the default may be a captured one."""
+    a, b = (torch.randint(0, 256, (r, 16 * 20), dtype=torch.uint8, device=DEV) for r in (1800, 1900))
+    sa, sb = (torch.randint(118, 126, (r, 20), dtype=torch.uint8, device=DEV) for r in (1800, 1900))
+    out, want = (torch.empty(1800, 1900, dtype=torch.float16, device=DEV) for _ in range(2))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        zdp.mx_product(a, sa, b, sb, out)
+    zdp.mx_product(a, sa, b, sb, want)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
 @pytest.mark.parametrize("m, n, kb", [(3, 40, 5), (70, 90, 20), (300, 520, 33)])
 def test_product_nan_blocks_and_extreme_scales(m, n, kb):
     g = np.random.default_rng(kb)

@@ -580,9 +580,10 @@ def _mx_types():
 
 def _device_of(t, name):
     """The index of the device a tensor is on."""
-    if not isinstance(t, _mx().tensor) or not t.is_cuda:
+    dev = t.get_device() if isinstance(t, _mx().tensor) else -1
+    if dev < 0 or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    return t.get_device()
+    return dev
 
 
 def _call(fn, device, stream, *args):
@@ -617,6 +618,8 @@ def _need_rows(t, name, dtypes, device):
     if len(shape) != 2:
         raise ValueError(f"{name}: {len(shape)} dimensions, expected 2")
     rows, cols = shape
+    if t.is_contiguous():
+        return rows, cols, cols
     s0, s1 = t.stride()
     if s1 != 1 and cols > 1:
         raise ValueError(f"{name}: its rows are not dense")
@@ -629,7 +632,17 @@ def _need_rows(t, name, dtypes, device):
 
 def _need_mx(codes, scales, name, device, rows=None, values=None):
     """(rows, blocks a row, blocks from row to row) of a 4-bit matrix (2-D codes and scales)."""
-    u8 = (_mx().u8,)
+    u8 = _mx().u8
+    try:  # the common case in few look-ups: dense, and nothing wrong
+        if (codes.dtype is u8 and scales.dtype is u8 and codes.get_device() == device == scales.get_device()
+                and codes.is_contiguous() and scales.is_contiguous()):
+            r, kb = scales.shape
+            if (codes.shape == (r, 16 * kb) and (rows is None or r == rows)
+                    and (values is None or kb == -(-values // MX_BLOCK))):
+                return r, kb, kb
+    except (AttributeError, TypeError, ValueError):
+        pass  # what follows says what is wrong
+    u8 = (u8,)
     rc, cc, ld_c = _need_rows(codes, name, u8, device)
     r, kb, ld = _need_rows(scales, name, u8, device)
     if rc != r or cc != 16 * kb:
