@@ -67,6 +67,7 @@ __device__ __forceinline__ void store16(void* p, u4 x, int64_t left) {
 // Quantise along the rows. Item i is part i % kLanes of block i / kLanes, blocks
 // counted row by row. FLAT: one row (a shard, or a dense matrix of whole
 // blocks); a full tile's loads are then all in flight before the first is used.
+// Bound by HBM: 117M fp32 values 87 us (6.1 TB/s), bf16 47 (6.3).
 // ------------------------------------------------------------------------
 
 template <int DT, bool FLAT>
@@ -112,6 +113,8 @@ __global__ void __launch_bounds__(kBlock) mx_quantize_rows_kernel(const MxQuantA
 // in LDS in their own type, and then takes every column's four blocks of 32
 // from there. 128 values either way make a tile's codes 64 contiguous bytes of
 // every row and of every column.
+// Bound by HBM and by its pieces of 64 bytes: 8192 x 14336 bf16 77-87 us (4.2-4.8
+// TB/s), fp32 125.
 // LDS holds rows of dwords (two 16-bit values or one fp32 value each); dword c
 // of row i stands at c ^ 16 * (i / 32). A wave's column reads take 16
 // neighbouring dwords of four rows that are 32 rows apart, and the permutation
@@ -269,6 +272,7 @@ __device__ __forceinline__ u4 widen(uint32_t c, uint32_t byte) {
   return w;
 }
 
+// Bound by HBM: 117M values to bf16 43 us (6.9 TB/s), to fp32 75 (7.1).
 template <int DT, bool FLAT>
 __global__ void __launch_bounds__(kBlock) mx_widen_kernel(const MxWidenArgs W) {
   using R = Raw<DT>;
@@ -310,7 +314,9 @@ __global__ void __launch_bounds__(kBlock) mx_widen_kernel(const MxWidenArgs W) {
 // Average of the N_d copies, and the norm / overflow partials of the unscaled
 // gradient (as the 16-bit averaging pass). A lane takes quads of values, the
 // loads of up to eight copies of all its quads in flight at once; the additions
-// stay in the copies' order.
+// stay in the copies' order. Bound by HBM: 8 copies of 117M values 161 us (6.0
+// TB/s); with 2 quads a lane or 4 copies at a time 166-170, codes without the
+// non-temporal hint 168.
 // ------------------------------------------------------------------------
 
 constexpr int kReduceQuads = 4;
@@ -326,7 +332,7 @@ __device__ __forceinline__ void add_copies(const MxCopies& S, int r, const int64
     const uint8_t* scales = S.strided ? S.scales[0] + (r + q) * S.scale_stride : S.scales[r + q];
 #pragma unroll
     for (int k = 0; k < kReduceQuads; ++k) {
-      c[q][k] = reinterpret_cast<const uint16_t*>(codes)[at[k]];
+      c[q][k] = ld_stream(reinterpret_cast<const uint16_t*>(codes) + at[k]);
       e[q][k] = scales[at[k] / kQuadLanes];
     }
   }
