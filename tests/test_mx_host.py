@@ -207,6 +207,14 @@ def test_view_of_a_tensor_in_a_flat_vector():
             zdp.mx_view(c, s, *bad)
 
 
+@pytest.mark.parametrize("bad", [(0, -1, 32), (64, -2, 96), (0, 1, -32), (64, -1, -32)])
+def test_view_of_fewer_than_no_values_is_refused(bad):
+    """Slices with a negative end would silently be the vector without its last blocks."""
+    c, s = torch.zeros(16 * 12, dtype=torch.uint8), torch.zeros(12, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        zdp.mx_view(c, s, *bad)
+
+
 def test_the_plain_form_is_the_nearest_code():
     """Brute force: every code's value against the plain form's choice."""
     rng = np.random.default_rng(1)

@@ -545,6 +545,8 @@ def mx_view(codes, scales, offset, rows, cols):
     multiples of 32 (its rows are then whole blocks)."""
     if offset < 0 or offset % MX_BLOCK or cols % MX_BLOCK:
         raise ValueError(f"offset {offset} and cols {cols} must be multiples of {MX_BLOCK}")
+    if rows < 0 or cols < 0:
+        raise ValueError(f"rows {rows} and cols {cols} must not be negative")
     b, n = offset // MX_BLOCK, rows * cols // MX_BLOCK
     if codes.dim() != 1 or scales.dim() != 1 or scales.numel() < b + n or codes.numel() < 16 * (b + n):
         raise ValueError("the tensor does not lie inside the flat vector")
