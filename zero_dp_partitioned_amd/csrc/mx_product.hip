@@ -313,9 +313,9 @@ __global__ void __launch_bounds__(64 * NW) mx_product_split_kernel(const MxProdu
 // 4096 instead of 274). The loop holds no branch that the compiler sees
 // (fetch_to_lds_if).
 //
-// Measured at 8192 x 14336 x 4096 with bf16 output: 250-266 us, 3.6-3.8
+// Measured at 8192 x 14336 x 4096 with bf16 output: 244-255 us, 3.8-3.9
 // PFLOP/s; the instruction alone reaches 6.4 on random codes and 5.6 with its
-// operands read from LDS (power holds the clock at 1.75-1.85 GHz). 8 waves of
+// operands read from LDS (power holds the clock at 1.85 GHz). 8 waves of
 // 128 x 64 beat 4 of 128 x 128 (274), whose one wave per SIMD shows every wait.
 // ------------------------------------------------------------------------
 

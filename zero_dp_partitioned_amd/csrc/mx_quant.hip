@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kBlock) mx_quantize_rows_kernel(const MxQuantA
 // in LDS in their own type, and then takes every column's four blocks of 32
 // from there. 128 values either way make a tile's codes 64 contiguous bytes of
 // every row and of every column.
-// Bound by HBM and by its pieces of 64 bytes: 8192 x 14336 bf16 77-87 us (4.2-4.8
+// Bound by HBM and by its pieces of 64 bytes: 8192 x 14336 bf16 74-78 us (4.6-4.8
 // TB/s), fp32 125.
 // LDS holds rows of dwords (two 16-bit values or one fp32 value each); dword c
 // of row i stands at c ^ 16 * (i / 32). A wave's column reads take 16
