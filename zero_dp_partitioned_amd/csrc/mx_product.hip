@@ -150,15 +150,16 @@ __device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
 }
 
 // Fetch 16 bytes a lane from base + off into LDS at `lds` + 16 * lane. No vector
-// register is written; the caller waits on vmcnt. (m0 is no register the
-// compiler allocates: it sets it right before each use of its own.)
+// register is written; the caller waits on vmcnt. The hardware wants one wait
+// state between the write of m0 and the load that takes its LDS base from it;
+// inside an asm the compiler puts none in.
 __device__ __forceinline__ void fetch_to_lds(const uint8_t* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
 }
 
 // The same if i < n (uniform). The branch is the asm's own: one that the
 // compiler sees splits the loop around it, and its accumulators are then kept
-// twice.
+// twice. The compare and the branch are the wait states.
 __device__ __forceinline__ void fetch_to_lds_if(uint32_t i, uint32_t n, const uint8_t* base, uint32_t off, uint32_t lds) {
   asm volatile(
       "s_mov_b32 m0, %0\n\ts_cmp_ge_u32 %3, %4\n\ts_cbranch_scc1 .Lzdp_skip%=\n\t"
