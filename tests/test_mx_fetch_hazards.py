@@ -79,6 +79,15 @@ def test_the_reader_finds_planted_hazards():
         assert n == 1 and bool(early) == found, text
 
 
+def test_every_asm_that_writes_m0_says_so():
+    """What an asm overwrites stands in its list, or the compiler may keep a value there across it."""
+    with open(os.path.join(build.CSRC, "mx_product.hip")) as f:
+        blocks = [b for b in re.findall(r"\basm volatile\((.*?)\);", f.read(), re.S) if re.search(r"\bm0,", b)]
+    assert len(blocks) == 2
+    for b in blocks:
+        assert '"m0"' in b.rsplit(":", 1)[1], b
+
+
 def test_every_fetch_to_lds_keeps_its_wait_states(tmp_path):
     out = tmp_path / "mx_product.s"
     cmd = [build.hipcc(), *build.COMMON, *build.DEVICE, "-x", "hip", "--cuda-device-only", "-S",

@@ -149,12 +149,19 @@ __device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const uint8_t*)p));
 }
 
+// m0 is named as overwritten, so that the compiler keeps no value of its own
+// there across a fetch. It warns about every such list because it reserves m0
+// and cannot save it; nothing needs it saved.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+
 // Fetch 16 bytes a lane from base + off into LDS at `lds` + 16 * lane. No vector
 // register is written; the caller waits on vmcnt. The hardware wants one wait
 // state between the write of m0 and the load that takes its LDS base from it;
 // inside an asm the compiler puts none in.
 __device__ __forceinline__ void fetch_to_lds(const uint8_t* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
 }
 
 // The same if i < n (uniform). The branch is the asm's own: one that the
@@ -164,8 +171,10 @@ __device__ __forceinline__ void fetch_to_lds_if(uint32_t i, uint32_t n, const ui
   asm volatile(
       "s_mov_b32 m0, %0\n\ts_cmp_ge_u32 %3, %4\n\ts_cbranch_scc1 .Lzdp_skip%=\n\t"
       "global_load_lds_dwordx4 %1, %2\n.Lzdp_skip%=:" ::"s"(lds), "v"(off), "s"(base), "s"(i), "s"(n)
-      : "memory", "scc");
+      : "memory", "scc", "m0");
 }
+
+#pragma clang diagnostic pop
 
 // ------------------------------------------------------------------------
 // Few output tiles: a block owns an output tile of 32 FM x 32 FN and its waves
