@@ -754,3 +754,19 @@ def test_refusals_on_the_device():
         zdp.mx_reduce_grad_segment([flat_c], [], torch.empty(8, device=DEV), ws, 0, st)
     with pytest.raises(ValueError):
         zdp.mx_reduce_grad_segment([flat_c], [flat_s], torch.empty(300, device=DEV), ws, 0, st)
+
+
+def test_a_matrix_in_the_place_of_a_flat_vector_is_refused():
+    """Rows of 40 values are padded to 64: none of the flat calls reads or writes them as 1,280 values in a row."""
+    c, s = zdp.mx_empty(32, 40)
+    marked = [t.fill_(0xA5) for t in (c, s)]
+    out = torch.full((1280,), 3.0, device=DEV)
+    st, ws = zdp.new_state(), zdp.new_workspace(1)
+    for codes, scales in ((c, s), (c.view(-1), s), (c, s.view(-1))):
+        with pytest.raises(ValueError, match="dimensions"):
+            zdp.mx_dequantize(codes, scales, out)
+        with pytest.raises(ValueError, match="dimensions"):
+            zdp.mx_cast_writeback(torch.zeros(1280, device=DEV), codes, scales)
+        with pytest.raises(ValueError, match="dimensions"):
+            zdp.mx_reduce_grad_segment([codes], [scales], out, ws, 0, st)
+    assert (out == 3.0).all() and all((t == 0xA5).all() for t in marked)

@@ -242,3 +242,16 @@ def test_the_plain_form_at_the_edges():
     v = _mx.decode(codes, scales)
     assert v[2, 0] == 6 * 2.0 ** 125 and np.isnan(v[3]).all() and np.isnan(v[4]).all()
     assert v[5, :8].tolist() == [4.0, 2.0, 4.0, 0.0, 1.0, 1.0, 2.0, -6.0]
+
+
+def test_a_matrix_is_no_flat_vector():
+    """The rows of a 32 x 40 matrix are padded to whole blocks: read as a vector, the padding would be values."""
+    dev = -1
+    c, s = _mx_tensors(32, 2)
+    f = zdp._need_flat
+    for codes, scales in ((c, s), (c.view(-1), s), (c, s.view(-1)), (c.view(4, 8, 32), s.view(-1))):
+        with pytest.raises(ValueError, match="dimensions"):
+            f(codes, scales, "v", dev, 0, 1280)
+    assert f(c.view(-1), s.view(-1), "v", dev, 0, 1280) == (40, 64)
+    with pytest.raises(ValueError, match="dimensions"):
+        f(torch.tensor(0, dtype=torch.uint8), s.view(-1), "v", dev, 0, 0)

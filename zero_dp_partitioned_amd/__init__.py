@@ -673,6 +673,8 @@ def _need_flat(codes, scales, name, device, offset, n):
     u8 = (_mx().u8,)
     nbytes = _need_values(codes, name, u8, device)
     blocks = _need_values(scales, name, u8, device)
+    if codes.dim() != 1 or scales.dim() != 1:  # a matrix pads its rows to whole blocks
+        raise ValueError(f"{name}: codes of {codes.dim()} and scales of {scales.dim()} dimensions, expected 1")
     if offset < 0 or offset % MX_BLOCK:
         raise ValueError(f"{name}: offset {offset} is not a multiple of {MX_BLOCK}")
     end = offset // MX_BLOCK + -(-n // MX_BLOCK)
@@ -747,8 +749,8 @@ def mx_reduce_grad_segment(codes, scales, avg_out, workspace, group, state, stre
     u8, kb = _mx().u8, -(-n // MX_BLOCK)
     for r, (c, s) in enumerate(zip(codes, scales)):
         if not (type(c) is type(s) is type(avg_out) and c.dtype == s.dtype == u8 and c.get_device() == dev
-                and s.get_device() == dev and c.is_contiguous() and s.is_contiguous() and s.numel() >= kb
-                and c.numel() >= 16 * kb):
+                and s.get_device() == dev and c.dim() == s.dim() == 1 and c.is_contiguous() and s.is_contiguous()
+                and s.numel() >= kb and c.numel() >= 16 * kb):
             _need_flat(c, s, f"copy {r}", dev, 0, n)  # says what is wrong, if anything
     _call(load().zero_mx_reduce_grad_segment, dev, stream, _ptr_array(codes), _ptr_array(scales), n_d, n,
           avg_out.data_ptr(), workspace.data_ptr(), _nbytes(workspace), group, state.data_ptr())
