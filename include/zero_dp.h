@@ -421,10 +421,14 @@ int zero_mx_reduce_grad_segment(const void* const* codes, const void* const* sca
 /* Product of two 4-bit matrices along their rows: for i < m, j < n
  *   out[i * ldo + j] = sum over k of A[i][k] * B[j][k],
  * A m x (32 * k_blocks) with lda blocks from row to row, B n x (32 * k_blocks)
- * with ldb. Products are exact, sums are fp32 (in an order that depends on the
+ * with ldb. Sums are fp32, subnormals included (in an order that depends on the
  * sizes only, so results repeat bit for bit), and out is rounded once to out_dt
- * (F32, or F16 / BF16 to nearest even). A NaN block makes every output of its
- * row NaN. k_blocks = 0 gives zeros. Of a linear layer with weight W (out x in)
+ * (F32, or F16 / BF16 to nearest even). A term a * b is exact where fp32 holds
+ * it. Below fp32's smallest step, 2^-149, parts of terms and of partial sums may
+ * be lost: at most 2^-148 per term of the contraction (scale bytes 0 and 0 give
+ * 0). Past fp32's largest value a term or partial sum gives inf or NaN, unless
+ * the terms summed with it at once bring it back. A NaN block makes every output
+ * of its row NaN. k_blocks = 0 gives zeros. Of a linear layer with weight W (out x in)
  * all three products have this form: y = x W^T from x and W along their rows,
  * dx = dy W from dy and the transposed copy of W, dW = dy^T x from the
  * transposed copies of dy and x.

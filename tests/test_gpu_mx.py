@@ -473,6 +473,38 @@ def test_product_overflow_to_infinity():
     assert torch.isposinf(half).all()
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("low", [-166, -158, -150, -142, -134, -126])
+@pytest.mark.parametrize("m, n, kb", [(3, 40, 5), (70, 90, 20), (300, 520, 33), (1700, 1600, 9), (3300, 3328, 11)])
+def test_product_terms_around_the_smallest_fp32_values(m, n, kb, low, dt):
+    """Terms whose scales multiply to 2^low to 2^(low + 6): below fp32's smallest value, among its subnormals, above.
+
+    To the bound of other products come up to 2^-149 for each term (what of it lies below fp32's smallest step) and as
+    much again for each of at most as many additions (a subnormal sum rounded or cut)."""
+    g = np.random.default_rng(m - low)
+    lo = (254 + low) // 2
+    a, b = _mx.random_mx(g, m, kb, lo, lo + 4), _mx.random_mx(g, n, kb, 254 + low - lo, 254 + low - lo + 4)
+    out = torch.full((m, n), 9.0, dtype=DTS[dt], device=DEV)
+    zdp.mx_product(*(_up(t) for t in (*a, *b)), out)
+    a64, b64 = (torch.from_numpy(_mx.decode(*t)).to(DEV) for t in (a, b))
+    ref, size, k = a64 @ b64.t(), a64.abs() @ b64.abs().t(), 32 * kb
+    bound = k * 2.0 ** -23 * size + 2 * k * 2.0 ** -149
+    bound = bound + HALF_STEP[dt] * (ref.abs() + bound) + TINY[dt]
+    err = (out.double() - ref).abs()
+    assert (err <= bound).all(), f"worst {float((err / bound).max())} of the bound"
+    if low >= (-142 if dt == "f32" else -134):  # most outputs lie well above the smallest step of their type
+        assert float(((out.double() - ref).abs() < ref.abs()).double().mean()) > 0.9
+    if low <= -150:
+        assert float(out.double().abs().max()) < 2.0 ** -126, "no subnormal sums"
+
+
+def test_product_of_the_smallest_scales_is_zero():
+    c, s = np.full((40, 32), 0x77, np.uint8), np.zeros((40, 2), np.uint8)
+    out = torch.full((40, 40), 9.0, device=DEV)
+    zdp.mx_product(_up(c), _up(s), _up(c), _up(s), out)
+    assert (out == 0.0).all()  # 64 * 36 * 2^-254
+
+
 @pytest.mark.parametrize("m, n, kb", [(0, 5, 2), (5, 0, 2), (4, 6, 0), (300, 300, 0)])
 def test_empty_products(m, n, kb):
     out = torch.full((m, n), 3.0, device=DEV)
