@@ -108,6 +108,48 @@ def test_quantize_strided(rows, cols, off, ld, dt):
         assert (t[:, used:] == 0xA5).all(), "blocks past a row's last one were written"
 
 
+# Scale bytes that the largest magnitudes of each type reach, subnormal values included (byte 0 also stands for all below).
+BYTES = {"f32": range(0, 253), "f16": range(101, 139), "bf16": range(0, 253)}
+
+
+def _every_scale(dt):
+    """[rows, 64] values of the type: for every scale byte eight rows whose blocks' largest magnitude is 4 to 8 times the
+    scale, in sixteenths of it (ties and saturation among them); rows below byte 0; and rows of the smallest subnormal."""
+    g = np.random.default_rng(21)
+    e = np.repeat(np.arange(BYTES[dt][0] - (24 if BYTES[dt][0] == 0 else 0), BYTES[dt][-1] + 1), 8) - 127
+    x = g.integers(-127, 128, (e.size, 64)) / 16.0
+    for block in (0, 32):
+        x[np.arange(e.size), block + g.integers(0, 32, e.size)] = g.integers(64, 128, e.size) / 16.0
+    x = np.concatenate([np.ldexp(x, e[:, None]), g.choice([-TINY[dt], 0.0, TINY[dt]], (4, 64))])
+    return torch.from_numpy(x).to(DTS[dt])
+
+
+@pytest.mark.parametrize("dt", list(DTS))
+def test_quantize_under_every_scale(dt):
+    """Every scale byte with codes of every magnitude, from subnormal inputs to the type's largest, in each kernel."""
+    x = _every_scale(dt)
+    assert torch.isfinite(x).all()
+    want = _mx.quantize(x.double().numpy())
+    assert set(want[1].reshape(-1)) == set(BYTES[dt])
+    for byte in BYTES[dt][4 if dt == "f16" else 0:]:  # fp16's smallest values are too coarse for every code
+        codes = want[0].reshape(-1, 16)[want[1].reshape(-1) == byte]
+        assert len(set(np.concatenate([codes & 15, codes >> 4]).reshape(-1)) - {0, 8}) == 14, f"codes at byte {byte}"
+    rows = x.shape[0]
+    for buf in (x.to(DEV), torch.cat([x, x], 1).to(DEV)[:, :64]):  # dense; rows inside a wider array
+        c, s = zdp.mx_empty(rows, 64)
+        zdp.mx_quantize(buf, c, s)
+        _check_mx(c, s, want, "rows")
+    for both in (False, True):
+        ct, st = zdp.mx_empty(rows, 64)
+        other = zdp.mx_empty(64, rows) if both else (None, None)
+        zdp.mx_quantize(x.t().contiguous().to(DEV), *other, ct, st)
+        _check_mx(ct, st, want, "columns")
+    if dt == "f32":
+        fc, fs = (t.view(-1) for t in zdp.mx_empty(1, x.numel()))
+        zdp.mx_cast_writeback(x.view(-1).to(DEV), fc, fs)
+        _check_mx(fc, fs, (want[0].reshape(-1), want[1].reshape(-1)), "flat")
+
+
 @pytest.mark.parametrize("n", [1, 7, 31, 32, 33, 4095, 8192, 8193, 196_899, 1_048_577])
 @pytest.mark.parametrize("shift", [0, 1])
 def test_cast_writeback(n, shift):
