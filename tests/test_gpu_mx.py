@@ -108,6 +108,76 @@ def test_quantize_strided(rows, cols, off, ld, dt):
         assert (t[:, used:] == 0xA5).all(), "blocks past a row's last one were written"
 
 
+def _ordinary(rows, cols, dt, seed, special=None):
+    """Values without zero blocks, some of them ties; `special` stands in the first value only."""
+    g = np.random.default_rng(seed)
+    x = g.normal(size=(rows, cols)) * np.exp2(g.integers(-9, 6, (rows, 1)))
+    x.reshape(-1)[g.integers(0, x.size, x.size // 8)] = g.choice([-2.5, 0.25, 0.75, 1.75, 3.5, -5.0])
+    if special is not None:
+        x[0, 0] = special
+    return torch.from_numpy(x).to(DTS[dt])
+
+
+def _codes_where(want, nan):
+    """The expected blocks are NaN blocks where `nan` says so, and every other one, a partial one too, has codes."""
+    codes, scales = want
+    np.testing.assert_array_equal(scales == 255, nan)
+    np.testing.assert_array_equal((codes.reshape(*scales.shape, 16) & 0x77).any(-1), ~nan)
+
+
+FILLED = SHAPES + [(1, 2), (1, 7), (1, 63), (1, 65), (31, 1), (33, 1), (31, 33), (65, 2)]
+FILLED = [(r, c, None) for r, c in FILLED] + [(r, c, v) for r, c in FILLED if r > 32 < c for v in (np.inf, np.nan)]
+
+
+@pytest.mark.parametrize("dt", list(DTS))
+@pytest.mark.parametrize("rows, cols, special", FILLED)
+def test_quantize_with_codes_in_every_block(rows, cols, special, dt):
+    """Ragged sizes with something to get wrong in each block: one special value at most, where there are more blocks."""
+    x = _ordinary(rows, cols, dt, rows * 5 + cols, special)
+    want, want_t = _mx.quantize(x.double().numpy()), _mx.quantize(x.double().numpy().T)
+    nan = [np.zeros(w[1].shape, bool) for w in (want, want_t)]
+    if special is not None:
+        nan[0][0, 0] = nan[1][0, 0] = True
+    _codes_where(want, nan[0])
+    _codes_where(want_t, nan[1])
+    x = x.to(DEV)
+    c, s = zdp.mx_empty(rows, cols)
+    zdp.mx_quantize(x, c, s)
+    _check_mx(c, s, want, "rows")
+    ct, st = zdp.mx_empty(cols, rows)
+    zdp.mx_quantize(x, codes_t=ct, scales_t=st)
+    _check_mx(ct, st, want_t, "columns")
+    for t in (c, s, ct, st):
+        t.fill_(0x5A)
+    zdp.mx_quantize(x, c, s, ct, st)
+    _check_mx(c, s, want, "both, rows")
+    _check_mx(ct, st, want_t, "both, columns")
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 5, 7, 31, 32, 33, 34, 63, 64, 65, 1023, 1025, 4095, 4097])
+@pytest.mark.parametrize("shift", [0, 1, 2, 3])
+def test_cast_writeback_with_codes_in_every_block(n, shift):
+    """Short slices from masters at every 4-byte alignment, written and widened again."""
+    x = _ordinary(1, n + shift, "f32", n)[0, shift:]
+    want = _mx.quantize(x.double().numpy()[None])
+    _codes_where(want, np.zeros(want[1].shape, bool))
+    b0, b = 2, _mx.blocks(n)
+    c = torch.full((16 * (b0 + b),), 0xA5, dtype=torch.uint8, device=DEV)
+    s = torch.full((b0 + b,), 0xA5, dtype=torch.uint8, device=DEV)
+    base = torch.full((n + 8,), float("nan"), device=DEV)  # what stands around the master is not read into it
+    master = base[shift:shift + n]
+    master.copy_(x)
+    zdp.mx_cast_writeback(master, c, s, 32 * b0)
+    np.testing.assert_array_equal(_down(s)[b0:], want[1][0])
+    np.testing.assert_array_equal(_down(c)[16 * b0:], want[0][0])
+    assert (c[:16 * b0] == 0xA5).all() and (s[:b0] == 0xA5).all()
+    for dt in DTS:
+        out = torch.empty(n, dtype=DTS[dt], device=DEV)
+        zdp.mx_dequantize(c, s, out, offset=32 * b0)
+        v = torch.from_numpy(_mx.decode(*want)[0, :n]).to(DTS[dt])
+        assert torch.equal(out.cpu(), v) and torch.isfinite(v).all()
+
+
 # Scale bytes that the largest magnitudes of each type reach, subnormal values included (byte 0 also stands for all below).
 BYTES = {"f32": range(0, 253), "f16": range(101, 139), "bf16": range(0, 253)}
 
