@@ -9,6 +9,10 @@ any order and with truncation its error is at most K * 2^-23 * sum |a b|; the
 output's rounding adds half a step of its type. The rounding of a sum grows with
 the root of K in practice: the relative 2-norm of the error is held to 1e-6 for
 fp32 outputs as well."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -558,6 +562,13 @@ def test_captured_without_a_call_before():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+def test_first_calls_of_a_process_are_captured():
+    """Every variant, in a process where no call came before the capture."""
+    script = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_mx_first_capture.py")
+    r = subprocess.run([sys.executable, script], capture_output=True, text=True, timeout=110)
+    assert r.returncode == 0 and "first calls captured: ok" in r.stdout, r.stdout[-1000:] + r.stderr[-3000:]
 
 
 @pytest.mark.parametrize("m, n, kb", [(3, 40, 5), (70, 90, 20), (300, 520, 33)])
