@@ -2,6 +2,8 @@
 library and in the binding) fire before anything touches a device, and the
 plain numpy form the GPU tests compare with has the format's properties."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -9,6 +11,7 @@ import torch
 
 import _mx
 import zero_dp_partitioned_amd as zdp
+from zero_dp_partitioned_amd import build
 
 A = 1 << 20  # an aligned address that is never read: the checks come first
 BIG = 2 ** 62
@@ -255,3 +258,20 @@ def test_a_matrix_is_no_flat_vector():
     assert f(c.view(-1), s.view(-1), "v", dev, 0, 1280) == (40, 64)
     with pytest.raises(ValueError, match="dimensions"):
         f(torch.tensor(0, dtype=torch.uint8), s.view(-1), "v", dev, 0, 0)
+
+
+def _functions(path):
+    """{name: text} of the functions of a source file that begin in the first column."""
+    with open(path) as f:
+        text = f.read()
+    return {m[2]: m[0] for m in re.finditer(r"^(template <[^\n]*>\n)?\w[^\n;]*?\b(\w+)\([^;{]*\{\n.*?^\}", text, re.S | re.M)}
+
+
+def test_the_pieces_kept_twice_are_the_same():
+    """mx_device.h repeats what kernels.hip keeps to itself (encodings, norm partials): a change to one is a change to
+    both, or the 4-bit average's norm and flag are no longer those of the 16-bit one."""
+    mine, steps = (_functions(os.path.join(build.CSRC, f)) for f in ("mx_device.h", "kernels.hip"))
+    both = set(mine) & set(steps)
+    assert both >= {"ld_stream", "st_stream", "decode16", "encode16", "account", "write_block_partial", "route_partials"}
+    for name in sorted(both):
+        assert mine[name] == steps[name], f"{name} differs between mx_device.h and kernels.hip"
