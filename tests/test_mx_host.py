@@ -275,3 +275,17 @@ def test_the_pieces_kept_twice_are_the_same():
     assert both >= {"ld_stream", "st_stream", "decode16", "encode16", "account", "write_block_partial", "route_partials"}
     for name in sorted(both):
         assert mine[name] == steps[name], f"{name} differs between mx_device.h and kernels.hip"
+
+
+def test_the_binding_does_without_torch_s_private_names(monkeypatch):
+    """The 4-bit calls find the current device and stream through torch's public calls where it lacks the faster ones."""
+    class Stream:
+        def __init__(self, device):
+            self.cuda_stream = 70 + device
+
+    for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+        monkeypatch.delattr(torch._C, name)
+    monkeypatch.setattr(torch.cuda, "current_stream", Stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    types = zdp._MxTypes()
+    assert types.stream(2) == 72 and types.device() == 3
