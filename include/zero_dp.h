@@ -398,9 +398,9 @@ int zero_mx_quantize(const void* src, int32_t src_dt, int64_t rows, int64_t cols
                      void* scales, int64_t ld, void* codes_t, void* scales_t, int64_t ld_t, void* stream);
 
 /* The values of a 4-bit matrix: out[i * out_ld + j] = code * scale for j < cols,
- * rounded once to out_dt (exact in BF16 and, short of overflow to inf at the
- * largest scales, in F32; F16 rounds to nearest even). A NaN block gives the
- * canonical quiet NaN. A flat slice is one row (codes and scales at its first
+ * rounded once to out_dt: exact in F32 and BF16, but for the largest codes under
+ * the scale bytes 253 and 254, which overflow to inf; F16 rounds to nearest even,
+ * past its largest value to inf. A NaN block gives the canonical quiet NaN. A flat slice is one row (codes and scales at its first
  * block).
  * Errors: INVALID_ARG, ALIGNMENT. */
 int zero_mx_dequantize(const void* codes, const void* scales, int64_t rows, int64_t cols, int64_t ld, void* out,

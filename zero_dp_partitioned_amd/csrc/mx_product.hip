@@ -323,10 +323,14 @@ __global__ void __launch_bounds__(64 * NW) mx_product_split_kernel(const MxProdu
 // 4096 instead of 274). The loop holds no branch that the compiler sees
 // (fetch_to_lds_if).
 //
-// Measured at 8192 x 14336 x 4096 with bf16 output: 244-255 us, 3.8-3.9
+// Measured at 8192 x 14336 x 4096 with bf16 output: 243-256 us, 3.8-4.0
 // PFLOP/s; the instruction alone reaches 6.4 on random codes and 5.6 with its
-// operands read from LDS (power holds the clock at 1.85 GHz). 8 waves of
-// 128 x 64 beat 4 of 128 x 128 (274), whose one wave per SIMD shows every wait.
+// operands read from LDS (power holds the clock at 1.85 GHz there). With 4096 x
+// 4096 x 14336 (110.5 us where this took 247.5) that splits into 1.9 us a
+// stage, 4.6 PFLOP/s, and 5 us a tile that no product covers (prologue and
+// output; one block fills a CU's LDS): 37 of the 247 us. Between 3.9 and 5.6
+// the matrix pipes wait; power does not explain it. 8 waves of 128 x 64 beat 4
+// of 128 x 128 (274), whose one wave per SIMD shows every wait.
 // ------------------------------------------------------------------------
 
 constexpr int kGroupChunks = 4;

@@ -67,7 +67,10 @@ __device__ __forceinline__ void store16(void* p, u4 x, int64_t left) {
 // Quantise along the rows. Item i is part i % kLanes of block i / kLanes, blocks
 // counted row by row. FLAT: one row (a shard, or a dense matrix of whole
 // blocks); a full tile's loads are then all in flight before the first is used.
-// Bound by HBM: 117M fp32 values 87 us (6.1 TB/s), bf16 47 (6.3).
+// Bound by HBM: 117M fp32 values 87 us (6.1 TB/s), bf16 47 (6.3). Rows that are
+// not one after another or not whole blocks wait for each load in turn and
+// divide per item: 8192 x 14336 inside a wider array 103 us in fp32, 58 in bf16;
+// 8192 x 14335 93 and 54.
 // ------------------------------------------------------------------------
 
 template <int DT, bool FLAT>
@@ -113,8 +116,10 @@ __global__ void __launch_bounds__(kBlock) mx_quantize_rows_kernel(const MxQuantA
 // in LDS in their own type, and then takes every column's four blocks of 32
 // from there. 128 values either way make a tile's codes 64 contiguous bytes of
 // every row and of every column.
-// Bound by HBM and by its pieces of 64 bytes: 8192 x 14336 bf16 74-78 us (4.6-4.8
-// TB/s), fp32 125.
+// Bound by HBM traffic in the pieces of 64 bytes that this tile makes (half lines
+// of codes both ways: 135 MB written instead of 125; more rows a tile would make
+// whole lines of the columns' codes): 8192 x 14336 bf16 74-78 us (4.6-4.8 TB/s)
+// between other passes, 87 several in a row, fp32 125; 8192 x 14335 104 and 139.
 // LDS holds rows of dwords (two 16-bit values or one fp32 value each); dword c
 // of row i stands at c ^ 16 * (i / 32). A wave's column reads take 16
 // neighbouring dwords of four rows that are 32 rows apart, and the permutation
@@ -272,7 +277,9 @@ __device__ __forceinline__ u4 widen(uint32_t c, uint32_t byte) {
   return w;
 }
 
-// Bound by HBM: 117M values to bf16 43 us (6.9 TB/s), to fp32 75 (7.1).
+// Bound by HBM: 117M values to bf16 43 us (6.9 TB/s), to fp32 75 (7.1). Not FLAT:
+// 8192 x 14336 into a wider array 51 and 92, 8192 x 14335 (rows off 16 bytes) 57
+// and 111.
 template <int DT, bool FLAT>
 __global__ void __launch_bounds__(kBlock) mx_widen_kernel(const MxWidenArgs W) {
   using R = Raw<DT>;
@@ -316,7 +323,8 @@ __global__ void __launch_bounds__(kBlock) mx_widen_kernel(const MxWidenArgs W) {
 // loads of up to eight copies of all its quads in flight at once; the additions
 // stay in the copies' order. Bound by HBM: 8 copies of 117M values 161 us (6.0
 // TB/s); with 2 quads a lane or 4 copies at a time 166-170, codes without the
-// non-temporal hint 168.
+// non-temporal hint 168. Other counts of the same shard: 2 copies 131, 9 220, 16
+// 270 (5.4 TB/s), 64 1041, 65 (equally spaced) 1053 (4.3), 100 1701 (3.9).
 // ------------------------------------------------------------------------
 
 constexpr int kReduceQuads = 4;
