@@ -289,3 +289,18 @@ def test_the_binding_does_without_torch_s_private_names(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
     types = zdp._MxTypes()
     assert types.stream(2) == 72 and types.device() == 3
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """A launch goes to its stream's device, where the tensors' memory need not be mapped."""
+    class Stream:
+        def __init__(self, device):
+            self.device_index, self.cuda_stream = device, 7
+
+    calls = []
+    monkeypatch.setattr(zdp._mx(), "device", lambda: 0)
+    with pytest.raises(ValueError, match="device 1"):
+        zdp._call(lambda *a: calls.append(a) or zdp.OK, 0, Stream(1), 3)
+    assert not calls
+    zdp._call(lambda *a: calls.append(a) or zdp.OK, 0, Stream(0), 3)
+    assert calls == [(3, 7)]

@@ -593,7 +593,12 @@ def _device_of(t, name):
 def _call(fn, device, stream, *args):
     """Call an entry point on `device`'s current stream (or the one given), with that device current."""
     mx = _mx()
-    s = mx.stream(device) if stream is None else stream.cuda_stream
+    if stream is None:
+        s = mx.stream(device)
+    elif getattr(stream, "device_index", device) != device:  # the launch would go to the stream's device
+        raise ValueError(f"stream on device {stream.device_index}, tensors on device {device}")
+    else:
+        s = stream.cuda_stream
     if mx.device() == device:
         rc = fn(*args, s)
     else:
