@@ -1,0 +1,363 @@
+"""Cases of a residual feed-forward sublayer's operators, x + dropout(f(norm(x))), and their plain forms.
+
+Layer norm   y = (x - mean) * rstd * w + b over each row, rstd = 1 / sqrt(var + eps); its backward pass gives dx (plus the
+             residual stream's gradient), dw and db.
+Dropout      y = residual + keep * x / (1 - p). Element i is kept if word i % 4 of Philox4x32-10 (Salmon et al., 2011) with
+             the counter (i / 4, offset), low words first, and the key `seed` is at least round(p * 2^32). The backward
+             pass is the same operator on dy.
+Gated        h = act(x Wg^T) * (x Wu^T); with g and u the two products, its backward pass takes
+             dg = dh * act'(g) * u and du = dh * act(g) to dx = dg Wg + du Wu, dWg = dg^T x and dWu = du^T x.
+"""
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda"
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+BYTES = {"f32": 4, "f16": 2, "bf16": 2}
+EPS = 1e-5
+SEED = 0x5DEECE66D1234567
+
+
+# --------------------------------------------------------------------------
+# cases
+# --------------------------------------------------------------------------
+
+def listed():
+    return [
+        # one token at LLaMA-3 8B's width, while serving: launch-bound
+        {"name": "norm_token", "kind": "norm", "rows": 1, "cols": 4096, "dtype": "bf16", "train": False},
+        # 8 sequences of 1024 tokens at GPT-2 1.5B's width, mean and rstd kept for the backward pass
+        {"name": "norm_train", "kind": "norm", "rows": 8192, "cols": 1600, "dtype": "f16", "train": True},
+        # a ragged batch at the same width, fp16 gradients
+        {"name": "norm_backward_ragged", "kind": "norm_backward", "rows": 1001, "cols": 1600, "dtype": "f16",
+         "residual": False},
+        # 16384 tokens at 4096, the residual stream's gradient added on the way
+        {"name": "norm_backward_train", "kind": "norm_backward", "rows": 16384, "cols": 4096, "dtype": "bf16",
+         "residual": True},
+        # the smallest batch: 45 tokens at GPT-2 1.5B's width, with the residual
+        {"name": "dropout_batch", "kind": "dropout", "rows": 45, "cols": 1600, "dtype": "f16", "p": 0.1, "residual": True,
+         "first": 0},
+        # the backward pass of one rank's odd slice of an fp32 tensor: the mask of the whole, no residual
+        {"name": "dropout_slice", "kind": "dropout", "rows": 1001, "cols": 6400, "dtype": "f32", "p": 0.1,
+         "residual": False, "first": 6_406_401},
+        # 16384 tokens at 4096 with the residual
+        {"name": "dropout_train", "kind": "dropout", "rows": 16384, "cols": 4096, "dtype": "bf16", "p": 0.1,
+         "residual": True, "first": 0},
+        # one token through LLaMA-3 8B's gate and up projections
+        {"name": "gated_token", "kind": "gated", "m": 1, "d": 4096, "f": 14336, "dtype": "bf16", "act": "silu",
+         "train": False},
+        # a decoding batch at GPT-2 1.5B's sizes
+        {"name": "gated_batch", "kind": "gated", "m": 45, "d": 1600, "f": 6400, "dtype": "f16", "act": "gelu_tanh",
+         "train": False},
+        # 8192 tokens, the two products kept for the backward pass
+        {"name": "gated_train", "kind": "gated", "m": 8192, "d": 4096, "f": 14336, "dtype": "bf16", "act": "silu",
+         "train": True},
+        # a ragged batch's gradients at GPT-2 1.5B's sizes
+        {"name": "gated_backward_ragged", "kind": "gated_backward", "m": 1001, "d": 1600, "f": 6400, "dtype": "f16",
+         "act": "gelu_tanh"},
+        # 8192 tokens' gradients
+        {"name": "gated_backward_train", "kind": "gated_backward", "m": 8192, "d": 4096, "f": 14336, "dtype": "bf16",
+         "act": "silu"},
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    kind = rng.choice(["norm", "norm_backward", "dropout", "gated", "gated_backward"])
+    if kind in ("norm", "norm_backward", "dropout"):
+        dtype = rng.choice(["f16", "bf16", "f32"])
+        cols = _log(rng, 32, 16384)
+        case = {"kind": kind, "rows": _log(rng, 1, min(65536, 16384 * 4096 // cols)), "cols": cols, "dtype": dtype}
+        if kind == "norm":
+            case["train"] = rng.random() < 0.5
+        elif kind == "norm_backward":
+            case["residual"] = rng.random() < 0.5
+        else:
+            case |= {"p": rng.choice([0.0, 0.05, 0.1, 0.5, 0.9]), "residual": rng.random() < 0.5,
+                     "first": rng.choice([0, rng.randrange(1 << 34)])}
+        return case
+    m, d = _log(rng, 1, 8192), _log(rng, 1, 8192)
+    case = {"kind": kind, "m": m, "d": d, "f": _log(rng, 1, min(28672, 8192 * 4096 * 14336 // (m * d))),
+            "dtype": rng.choice(["f16", "bf16"]), "act": rng.choice(["silu", "gelu", "gelu_tanh", "relu", "sigmoid"])}
+    if kind == "gated":
+        case["train"] = rng.random() < 0.5
+    return case
+
+
+def work(case):
+    kind, s = case["kind"], BYTES[case["dtype"]]
+    if kind == "norm":
+        n = case["rows"] * case["cols"]
+        return {"bytes": 2 * n * s + 2 * case["cols"] * s + (8 * case["rows"] if case["train"] else 0), "flops": 8 * n}
+    if kind == "norm_backward":
+        n = case["rows"] * case["cols"]
+        return {"bytes": (4 if case["residual"] else 3) * n * s + 3 * case["cols"] * s + 8 * case["rows"], "flops": 14 * n}
+    if kind == "dropout":  # the generator: 20 products of 32 bits and as many sums for four elements
+        n = case["rows"] * case["cols"]
+        return {"bytes": (3 if case["residual"] else 2) * n * s, "flops": 12 * n}
+    m, d, f = case["m"], case["d"], case["f"]
+    if kind == "gated":
+        return {"bytes": (m * d + 2 * f * d + (3 if case["train"] else 1) * m * f) * s, "flops": 4 * m * d * f}
+    return {"bytes": (2 * m * d + 4 * f * d + 3 * m * f) * s, "flops": 8 * m * d * f}
+
+
+# --------------------------------------------------------------------------
+# plain forms (fp32)
+# --------------------------------------------------------------------------
+
+def _words(n, first, seed, offset):
+    """Words [first, first + n) of the generator, as int64."""
+    low = 0xFFFFFFFF
+    block0 = first // 4
+    i = torch.arange(block0, (first + n + 3) // 4, device=DEV)
+    c = [i & low, i >> 32 & low, torch.full_like(i, offset & low), torch.full_like(i, offset >> 32 & low)]
+    k = [seed & low, seed >> 32 & low]
+    for _ in range(10):
+        # the products wrap past 2^63; their 64 bits are still right
+        a, b = c[0] * 0xD2511F53, c[2] * 0xCD9E8D57
+        c = [(b >> 32 & low) ^ c[1] ^ k[0], b & low, (a >> 32 & low) ^ c[3] ^ k[1], a & low]
+        k = [(k[0] + 0x9E3779B9) & low, (k[1] + 0xBB67AE85) & low]
+    return torch.stack(c, 1).reshape(-1)[first - 4 * block0:][:n]
+
+
+def _act(g, act):
+    if act == "silu":
+        return g / (1 + torch.exp(-g))
+    if act == "gelu":
+        return 0.5 * g * (1 + torch.erf(g / math.sqrt(2)))
+    if act == "gelu_tanh":
+        return 0.5 * g * (1 + torch.tanh(math.sqrt(2 / math.pi) * (g + 0.044715 * g ** 3)))
+    if act == "relu":
+        return torch.where(g > 0, g, 0.0)
+    return 1 / (1 + torch.exp(-g))
+
+
+def _act_grad(g, act):
+    if act == "silu":
+        s = 1 / (1 + torch.exp(-g))
+        return s * (1 + g * (1 - s))
+    if act == "gelu":
+        return 0.5 * (1 + torch.erf(g / math.sqrt(2))) + g * torch.exp(-0.5 * g * g) / math.sqrt(2 * math.pi)
+    if act == "gelu_tanh":
+        t = torch.tanh(math.sqrt(2 / math.pi) * (g + 0.044715 * g ** 3))
+        return 0.5 * (1 + t) + 0.5 * g * (1 - t * t) * math.sqrt(2 / math.pi) * (1 + 3 * 0.044715 * g * g)
+    if act == "relu":
+        return torch.where(g > 0, 1.0, 0.0)
+    s = 1 / (1 + torch.exp(-g))
+    return s * (1 - s)
+
+
+def _plain(s):
+    kind = s["kind"]
+    if kind == "norm":
+        x = s["x"].float()
+        mean = x.mean(1, keepdim=True)
+        rstd = 1 / torch.sqrt((x - mean).square().mean(1, keepdim=True) + EPS)
+        y = ((x - mean) * rstd * s["weight"].float() + s["bias"].float()).to(s["x"].dtype)
+        return [y, mean[:, 0], rstd[:, 0]] if s["train"] else y
+    if kind == "norm_backward":
+        x, dy, w = s["x"].float(), s["dy"].float(), s["weight"].float()
+        xhat = (x - s["mean"][:, None]) * s["rstd"][:, None]
+        v = dy * w
+        dx = s["rstd"][:, None] * (v - v.mean(1, keepdim=True) - xhat * (v * xhat).mean(1, keepdim=True))
+        if s["dresidual"] is not None:
+            dx = dx + s["dresidual"].float()
+        return [t.to(s["x"].dtype) for t in (dx, (dy * xhat).sum(0), dy.sum(0))]
+    if kind == "dropout":
+        x, p = s["x"].float(), s["p"]
+        keep = _words(x.numel(), s["first"], SEED, s["offset"]) >= round(p * 2 ** 32)
+        y = torch.where(keep.view(x.shape), x / (1 - p), 0.0)
+        if s["residual"] is not None:
+            y = y + s["residual"].float()
+        return y.to(s["x"].dtype)
+    x, wg, wu = s["x"].float(), s["w_gate"].float(), s["w_up"].float()
+    if kind == "gated":
+        g, u = x @ wg.t(), x @ wu.t()
+        got = [_act(g, s["act"]) * u] + ([g, u] if s["train"] else [])
+        return [t.to(s["x"].dtype) for t in got]
+    g, u, dh = s["gate"].float(), s["up"].float(), s["dh"].float()
+    dg, du = dh * _act_grad(g, s["act"]) * u, dh * _act(g, s["act"])
+    return [t.to(s["x"].dtype) for t in (dg @ wg + du @ wu, dg.t() @ x, du.t() @ x)]
+
+
+# --------------------------------------------------------------------------
+# the framework's calls
+# --------------------------------------------------------------------------
+
+def _kernels(s):
+    import zero_dp_partitioned_amd as zdp
+    kind = s["kind"]
+    if kind.endswith("_backward") and s["workspace"] is None:  # a program makes it once
+        s["workspace"] = zdp.new_workspace(1)
+    if kind == "norm":
+        if not s["train"]:
+            zdp.layer_norm(s["x"], s["weight"], s["bias"], s["y"], EPS)
+            return s["y"]
+        zdp.layer_norm(s["x"], s["weight"], s["bias"], s["y"], EPS, mean=s["mean"], rstd=s["rstd"])
+        return [s["y"], s["mean"], s["rstd"]]
+    if kind == "norm_backward":
+        zdp.layer_norm_backward(s["dy"], s["x"], s["weight"], s["mean"], s["rstd"], s["dx"], s["dweight"], s["dbias"],
+                                workspace=s["workspace"], dresidual=s["dresidual"])
+        return [s["dx"], s["dweight"], s["dbias"]]
+    if kind == "dropout":
+        zdp.dropout(s["x"], s["y"], s["p"], SEED, s["offset"], residual=s["residual"], first=s["first"])
+        return s["y"]
+    if kind == "gated":
+        zdp.gated_product(s["x"], s["w_gate"], s["w_up"], s["out"], s["act"], gate=s["gate"], up=s["up"])
+        return [s["out"]] + ([s["gate"], s["up"]] if s["train"] else [])
+    zdp.gated_product_backward(s["dh"], s["x"], s["w_gate"], s["w_up"], s["gate"], s["up"], s["dgate"], s["dup"],
+                               s["workspace"], dx=s["dx"], dw_gate=s["dw_gate"], dw_up=s["dw_up"], act=s["act"])
+    return [s["dx"], s["dw_gate"], s["dw_up"]]
+
+
+def run(state):
+    return _kernels(state) if own else _plain(state)
+
+
+# --------------------------------------------------------------------------
+# inputs
+# --------------------------------------------------------------------------
+
+def _normal(gen, *shape, sigma=1.0, dtype=torch.float32):
+    return (torch.randn(*shape, generator=gen, device=DEV) * sigma).to(dtype)
+
+
+def _stream(gen, rows, cols, dtype):
+    """A residual stream: tokens of several sizes, some channels far larger than the others, a shared offset."""
+    x = _normal(gen, rows, cols) + 0.3 * _normal(gen, 1, cols)
+    x[:, ::97] *= 12
+    return (x * torch.exp(0.5 * _normal(gen, rows, 1))).to(dtype)
+
+
+def _gradients(gen, rows, cols, dtype, sigma=0.05):
+    """Gradients times a loss scale, each token at its own size."""
+    return (_normal(gen, rows, cols, sigma=sigma) * torch.exp(0.5 * _normal(gen, rows, 1))).to(dtype)
+
+
+def _inputs(case, seed):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    kind, dt = case["kind"], TYPES[case["dtype"]]
+    if kind in ("norm", "norm_backward"):
+        rows, cols = case["rows"], case["cols"]
+        got = {"x": _stream(gen, rows, cols, dt), "weight": (1 + _normal(gen, cols, sigma=0.1)).to(dt),
+               "bias": _normal(gen, cols, sigma=0.02, dtype=dt)}
+        if kind == "norm_backward":
+            x = got["x"].double()
+            got["mean"] = x.mean(1).float()
+            got["rstd"] = torch.rsqrt(x.var(1, unbiased=False) + EPS).float()
+            got["dy"] = _gradients(gen, rows, cols, dt)
+            got["dresidual"] = _gradients(gen, rows, cols, dt) if case["residual"] else None
+        return got
+    if kind == "dropout":
+        rows, cols = case["rows"], case["cols"]
+        return {"x": _normal(gen, rows, cols, dtype=dt), "offset": seed & 0xFFFFFFFFFFFF,
+                "residual": _stream(gen, rows, cols, dt) if case["residual"] else None}
+    m, d, f = case["m"], case["d"], case["f"]
+    got = {"x": _normal(gen, m, d, dtype=dt), "w_gate": _normal(gen, f, d, sigma=0.02, dtype=dt),
+           "w_up": _normal(gen, f, d, sigma=0.02, dtype=dt)}
+    if kind == "gated_backward":
+        size = 0.02 * math.sqrt(d)  # of the products
+        got |= {"gate": _normal(gen, m, f, sigma=size, dtype=dt), "up": _normal(gen, m, f, sigma=size, dtype=dt),
+                "dh": _gradients(gen, m, f, dt)}
+    return got
+
+
+def prepare(case, seed):
+    kind = case["kind"]
+    s = {"kind": kind, **_inputs(case, seed)}
+    x = s["x"]
+    if kind == "norm":
+        s |= {"train": case["train"], "y": torch.empty_like(x)}
+        if case["train"]:
+            s |= {"mean": torch.empty(x.shape[0], device=DEV), "rstd": torch.empty(x.shape[0], device=DEV)}
+    elif kind == "norm_backward":
+        s |= {"dx": torch.empty_like(x), "dweight": torch.empty_like(s["weight"]), "dbias": torch.empty_like(s["weight"]),
+              "workspace": None}
+    elif kind == "dropout":
+        s |= {"p": case["p"], "first": case["first"], "y": torch.empty_like(x)}
+    elif kind == "gated":
+        m, f = case["m"], case["f"]
+        s |= {"act": case["act"], "train": case["train"], "out": x.new_empty(m, f),
+              "gate": x.new_empty(m, f) if case["train"] else None, "up": x.new_empty(m, f) if case["train"] else None}
+    else:
+        s |= {"act": case["act"], "dgate": torch.empty_like(s["gate"]), "dup": torch.empty_like(s["up"]),
+              "dx": torch.empty_like(x), "dw_gate": torch.empty_like(s["w_gate"]), "dw_up": torch.empty_like(s["w_up"]),
+              "workspace": None}
+    return s
+
+
+# --------------------------------------------------------------------------
+# the definition in 64 bits
+# --------------------------------------------------------------------------
+
+def _kept(n, first, p, offset):
+    """Whether elements [first, first + n) are kept. Products of 32 bits from 16-bit halves, so that nothing wraps."""
+    def times(c, m):
+        m0, m1, c0, c1 = m % 65536, m // 65536, c % 65536, c // 65536
+        middle = c0 * m0 // 65536 + c1 * m0 % 65536 + c0 * m1 % 65536
+        high = c1 * m1 + c1 * m0 // 65536 + c0 * m1 // 65536 + middle // 65536
+        return high, middle % 65536 * 65536 + c0 * m0 % 65536
+
+    index = torch.arange(first, first + n, device=DEV)
+    blocks, where = torch.unique_consecutive(index // 4, return_inverse=True)
+    x0, x1 = blocks % 2 ** 32, blocks // 2 ** 32
+    x2, x3 = torch.full_like(x0, offset % 2 ** 32), torch.full_like(x0, offset // 2 ** 32)
+    for r in range(10):
+        h0, l0 = times(x0, 0xD2511F53)
+        h1, l1 = times(x2, 0xCD9E8D57)
+        x0, x1, x2, x3 = (h1 ^ x1 ^ (SEED % 2 ** 32 + r * 0x9E3779B9) % 2 ** 32, l1,
+                          h0 ^ x3 ^ (SEED // 2 ** 32 + r * 0xBB67AE85) % 2 ** 32, l0)
+    limit, word = round(p * 2 ** 32), index % 4
+    return torch.where(word < 2, torch.where(word == 0, x0[where], x1[where]),
+                       torch.where(word == 2, x2[where], x3[where])) >= limit
+
+
+def _nonlinear(z, act):
+    """The activation and its derivative."""
+    if act == "relu":
+        return z.clamp_min(0), (z > 0).double()
+    if act in ("silu", "sigmoid"):
+        s = torch.sigmoid(z)
+        return (z * s, s + z * s * torch.sigmoid(-z)) if act == "silu" else (s, s * torch.sigmoid(-z))
+    if act == "gelu":
+        cdf = 0.5 * torch.erfc(-z * math.sqrt(0.5))
+        return z * cdf, cdf + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    # 0.5 (1 + tanh(a)) = sigmoid(2 a)
+    a2 = 2 * math.sqrt(2 / math.pi) * z * (1 + 0.044715 * z * z)
+    s = torch.sigmoid(a2)
+    return z * s, s + z * s * torch.sigmoid(-a2) * 2 * math.sqrt(2 / math.pi) * (1 + 0.134145 * z * z)
+
+
+def exact(case, seed):
+    s, kind = _inputs(case, seed), case["kind"]
+    s = {k: v.double() if torch.is_tensor(v) else v for k, v in s.items()}
+    x = s["x"]
+    if kind == "norm":
+        var, mean = torch.var_mean(x, 1, correction=0)
+        y = torch.addcmul(s["bias"], (x - mean[:, None]) / torch.sqrt(var + EPS)[:, None], s["weight"])
+        return [y, mean, torch.rsqrt(var + EPS)] if case["train"] else y
+    if kind == "norm_backward":
+        # the derivative's projection form: off the constants and off xhat
+        xhat = (x - s["mean"].unsqueeze(1)) * s["rstd"].unsqueeze(1)
+        v, n = s["dy"] * s["weight"], x.shape[1]
+        v = v - v.sum(1, keepdim=True) / n - torch.linalg.vecdot(v, xhat).unsqueeze(1) / n * xhat
+        dx = v * s["rstd"].unsqueeze(1)
+        if case["residual"]:
+            dx += s["dresidual"]
+        return [dx, torch.linalg.vecdot(s["dy"], xhat, dim=0), s["dy"].sum(0)]
+    if kind == "dropout":
+        y = x * _kept(x.numel(), case["first"], case["p"], s["offset"]).view(x.shape) / (1 - case["p"])
+        return y + s["residual"] if case["residual"] else y
+    wg, wu = s["w_gate"], s["w_up"]
+    if kind == "gated":
+        g, u = torch.mm(x, wg.t()), torch.mm(x, wu.t())
+        return [_nonlinear(g, case["act"])[0] * u] + ([g, u] if case["train"] else [])
+    a, da = _nonlinear(s["gate"], case["act"])
+    dg, du = s["dh"] * s["up"] * da, s["dh"] * a
+    return [torch.mm(torch.cat([dg, du], 1), torch.cat([wg, wu])), torch.mm(dg.t(), x), torch.mm(du.t(), x)]
