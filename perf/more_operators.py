@@ -82,8 +82,8 @@ def draw(rng):
             case |= {"p": rng.choice([0.0, 0.05, 0.1, 0.5, 0.9]), "residual": rng.random() < 0.5,
                      "first": rng.choice([0, rng.randrange(1 << 34)])}
         return case
-    m, d = _log(rng, 1, 8192), _log(rng, 1, 8192)
-    case = {"kind": kind, "m": m, "d": d, "f": _log(rng, 1, min(28672, 8192 * 4096 * 14336 // (m * d))),
+    m, d = _log(rng, 1, 8192), _log(rng, 64, 8192)
+    case = {"kind": kind, "m": m, "d": d, "f": _log(rng, 64, min(28672, 8192 * 4096 * 14336 // (m * d))),
             "dtype": rng.choice(["f16", "bf16"]), "act": rng.choice(["silu", "gelu", "gelu_tanh", "relu", "sigmoid"])}
     if kind == "gated":
         case["train"] = rng.random() < 0.5
