@@ -60,7 +60,7 @@ extern "C" {
 /* ---- dtypes (values are part of the ABI) -------------------------------- */
 #define ZERO_DT_F16 1  /* IEEE binary16 */
 #define ZERO_DT_BF16 2 /* bfloat16 */
-#define ZERO_DT_F32 3  /* fp32 (the zero_mx_* calls only) */
+#define ZERO_DT_F32 3  /* fp32 (the zero_mx_* calls and a layer's operators) */
 
 /* ---- microscaled 4-bit format (MXFP4) ------------------------------------
  * Blocks of ZERO_MX_BLOCK consecutive values share one scale byte (E8M0:
@@ -438,6 +438,59 @@ int zero_mx_reduce_grad_segment(const void* const* codes, const void* const* sca
 int zero_mx_product(const void* a_codes, const void* a_scales, int64_t lda, const void* b_codes, const void* b_scales,
                     int64_t ldb, int64_t m, int64_t n, int64_t k_blocks, void* out, int32_t out_dt, int64_t ldo,
                     void* stream);
+
+/* ---- a layer's operators ----------------------------------------------------
+ * What stands around the products of a residual sublayer, x + dropout(f(norm(x))),
+ * in training, on the step's buffers: weights are tensors of the 16-bit flat
+ * vector that the step writes, and their gradients go into the gradient copy that
+ * it reads. Not an operation of the pages. Tensors are rows of `cols` values, `ld`
+ * from row to row, aligned to their elements (16 bytes are not needed). Sums and
+ * statistics are fp32, in an order that depends on the sizes only, and every
+ * output is rounded once, to nearest even. A workspace is one of
+ * zero_workspace_bytes(); a call uses what the step's calls use only within one
+ * call, so it may run between them. Outputs must not overlap inputs or each
+ * other, but where a call says so. */
+
+/* Layer norm over each row of x (F32, F16 or BF16): with mean and var (the mean
+ * square of x - mean) of the row and rstd = 1 / sqrt(var + eps),
+ *   y = (x - mean) * rstd * weight + bias.
+ * weight and bias have `cols` values of w_dt: x's type or F32; bias may be NULL.
+ * mean and rstd (fp32, one a row, what the backward pass reads) are written unless
+ * both are NULL.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (more than 2^20 columns). */
+int zero_layer_norm(const void* x, int32_t dt, int64_t rows, int64_t cols, int64_t x_ld, const void* weight,
+                    const void* bias, int32_t w_dt, double eps, void* y, int64_t y_ld, float* mean, float* rstd,
+                    void* stream);
+
+/* Its backward pass. With xhat = (x - mean) * rstd and v = dy * weight,
+ *   dx = rstd * (v - mean(v) - xhat * mean(v * xhat)) + dresidual,
+ *   dweight = sum over rows of dy * xhat,   dbias = sum over rows of dy.
+ * dresidual (the residual stream's gradient, which joins here) may be NULL, and so
+ * may dweight and dbias, which are of dw_dt (F32, F16 or BF16). accumulate != 0
+ * adds both to what they hold. The workspace is needed for either of them.
+ * Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, UNSUPPORTED (more than 2^20 columns). */
+int zero_layer_norm_backward(const void* dy, int64_t dy_ld, const void* x, int64_t x_ld, int32_t dt, int64_t rows,
+                             int64_t cols, const void* weight, int32_t w_dt, const float* mean, const float* rstd,
+                             const void* dresidual, int64_t dresidual_ld, void* dx, int64_t dx_ld, void* dweight,
+                             void* dbias, int32_t dw_dt, int32_t accumulate, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* Dropout with a mask that is computed and never stored:
+ *   y = (kept ? x * fp32(1 / (1 - p)) : 0) + residual,   0 <= p < 1.
+ * Element e of the rows x cols (row by row) has the index i = first + e, and is
+ * kept if word i % 4 of Philox4x32-10 (Salmon et al., 2011), with the counter
+ * (low and high half of i / 4, low and high half of offset) and the key (low and
+ * high half of seed), is at least p * 2^32 rounded to an integer. So the backward pass is the same call on
+ * dy, without the residual, and a part of a larger tensor (a rank's slice, a
+ * micro-batch) gets the whole's mask through `first`. A dropped value is 0
+ * whatever it was. residual may be NULL. counter (a device int64, or NULL) is
+ * added to offset when the kernel runs: a captured graph draws another mask in
+ * every replay if something advances it. y may be x or residual (the same
+ * address and ld).
+ * Errors: INVALID_ARG, ALIGNMENT. */
+int zero_dropout(const void* x, int32_t dt, int64_t rows, int64_t cols, int64_t x_ld, const void* residual,
+                 int64_t residual_ld, void* y, int64_t y_ld, double p, uint64_t seed, uint64_t offset,
+                 const int64_t* counter, int64_t first, void* stream);
 
 /* ---- testing --------------------------------------------------------------
  * Not an operation of the pages. Caps the blocks of every streaming launch

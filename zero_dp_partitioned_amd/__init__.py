@@ -33,7 +33,8 @@ EXPORTS = ("zero_partition", "zero_partition_tensors", "zero_workspace_bytes",
            "zero_grad_norm_overflow", "zero_adam_step", "zero_cast_writeback", "zero_plan_arena",
            "zero_set_grid_limit", "zero_adam_step_static", "zero_copy_probe",
            "zero_mx_cast_writeback", "zero_mx_quantize", "zero_mx_dequantize",
-           "zero_mx_reduce_grad_segment", "zero_mx_product")
+           "zero_mx_reduce_grad_segment", "zero_mx_product",
+           "zero_layer_norm", "zero_layer_norm_backward", "zero_dropout")
 
 
 class ZeroError(RuntimeError):
@@ -135,6 +136,11 @@ def load():
         L.zero_mx_reduce_grad_segment.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(vp), i32, i64, vp, vp, sz, i32,
                                                   vp, vp]
         L.zero_mx_product.argtypes = [vp, vp, i64, vp, vp, i64, i64, i64, i64, vp, i32, i64, vp]
+        f64, u64 = ctypes.c_double, ctypes.c_uint64
+        L.zero_layer_norm.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, f64, vp, i64, vp, vp, vp]
+        L.zero_layer_norm_backward.argtypes = [vp, i64, vp, i64, i32, i64, i64, vp, i32, vp, vp, vp, i64, vp, i64, vp, vp,
+                                               i32, i32, vp, sz, vp]
+        L.zero_dropout.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i64, f64, u64, u64, vp, i64, vp]
         for name in EXPORTS:
             fn = getattr(L, name)
             if name not in ("zero_workspace_bytes", "zero_last_error"):
@@ -777,3 +783,119 @@ def mx_product(a_codes, a_scales, b_codes, b_scales, out, stream=None):
         raise ValueError(f"A has {kb} blocks a row, B {kb_b}")
     _call(load().zero_mx_product, dev, stream, a_codes.data_ptr(), a_scales.data_ptr(), lda, b_codes.data_ptr(),
           b_scales.data_ptr(), ldb, m, n, kb, out.data_ptr(), types[out.dtype], ldo)
+
+
+# --------------------------------------------------------------------------
+# a layer's operators around its products: 2-D tensors with dense rows, of any
+# distance from row to row; see include/zero_dp.h
+# --------------------------------------------------------------------------
+
+def _like(t, name, dtypes, device, rows, cols):
+    """The elements from row to row of a 2-D tensor of the given shape."""
+    r, c, ld = _need_rows(t, name, dtypes, device)
+    if r != rows or c != cols:
+        raise ValueError(f"{name}: {r} x {c}, expected {rows} x {cols}")
+    return ld
+
+
+def _vector(t, name, dtypes, device, n):
+    """The address of a dense vector of n values, or None for None."""
+    if t is None:
+        return None
+    if _need_values(t, name, dtypes, device) != n:
+        raise ValueError(f"{name}: {t.numel()} elements, expected {n}")
+    return t.data_ptr()
+
+
+def _scratch(workspace, device):
+    """(address, bytes) of a workspace (new_workspace)."""
+    if workspace is None:
+        raise ValueError("a workspace is needed (from new_workspace)")
+    _need_values(workspace, "workspace", (_mx().u8,), device)
+    return workspace.data_ptr(), workspace.numel()
+
+
+def _weight(weight, dev, dtype, cols):
+    types = _mx_types()
+    if weight is None:
+        raise TypeError("weight: a torch tensor is expected, got None")
+    return _vector(weight, "weight", (dtype, _mx().f32), dev, cols), types[weight.dtype]
+
+
+def layer_norm(x, weight, bias, y, eps=1e-5, mean=None, rstd=None, stream=None):
+    """y = (x - mean) * rstd * weight + bias over each row of x (fp32, fp16 or
+    bf16). weight and bias (or None) are of x's type or both fp32; mean and rstd
+    (fp32, one value a row) are written if given: the backward pass reads them."""
+    dev = _device_of(x, "x")
+    types, f32 = _mx_types(), (_mx().f32,)
+    rows, cols, x_ld = _need_rows(x, "x", types, dev)
+    y_ld = _like(y, "y", (x.dtype,), dev, rows, cols)
+    w, w_dt = _weight(weight, dev, x.dtype, cols)
+    b = _vector(bias, "bias", (weight.dtype,), dev, cols)
+    if (mean is None) != (rstd is None):
+        raise ValueError("mean and rstd must be given together")
+    _call(load().zero_layer_norm, dev, stream, x.data_ptr(), types[x.dtype], rows, cols, x_ld, w, b, w_dt, eps,
+          y.data_ptr(), y_ld, _vector(mean, "mean", f32, dev, rows), _vector(rstd, "rstd", f32, dev, rows))
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, workspace=None, dresidual=None,
+                        accumulate=False, stream=None):
+    """The gradients of layer_norm: dx (plus dresidual, the gradient that the
+    residual stream brings), and dweight and dbias (fp32, fp16 or bf16, both of
+    one type; either may be None), added to what they hold with `accumulate`.
+    Views into a flat gradient copy serve for both. They need a workspace."""
+    dev = _device_of(x, "x")
+    types, f32 = _mx_types(), (_mx().f32,)
+    rows, cols, x_ld = _need_rows(x, "x", types, dev)
+    one = (x.dtype,)
+    dy_ld, dx_ld = _like(dy, "dy", one, dev, rows, cols), _like(dx, "dx", one, dev, rows, cols)
+    w, w_dt = _weight(weight, dev, x.dtype, cols)
+    if mean is None or rstd is None:
+        raise TypeError("mean and rstd are needed (from layer_norm)")
+    res_ld = 0 if dresidual is None else _like(dresidual, "dresidual", one, dev, rows, cols)
+    dw, db = _vector(dweight, "dweight", types, dev, cols), None
+    if dbias is not None:
+        db = _vector(dbias, "dbias", types if dweight is None else (dweight.dtype,), dev, cols)
+    sums = dweight if dweight is not None else dbias
+    ws, ws_bytes = (None, 0) if sums is None else _scratch(workspace, dev)
+    _call(load().zero_layer_norm_backward, dev, stream, dy.data_ptr(), dy_ld, x.data_ptr(), x_ld, types[x.dtype], rows,
+          cols, w, w_dt, _vector(mean, "mean", f32, dev, rows), _vector(rstd, "rstd", f32, dev, rows),
+          None if dresidual is None else dresidual.data_ptr(), res_ld, dx.data_ptr(), dx_ld, dw, db,
+          0 if sums is None else types[sums.dtype], bool(accumulate), ws, ws_bytes)
+
+
+def dropout(x, y, p, seed, offset=0, residual=None, first=0, counter=None, stream=None):
+    """y = (kept ? x / (1 - p) : 0) + residual, for fp32, fp16 or bf16 tensors of
+    one shape: 2-D with dense rows, or contiguous with any number of dimensions.
+    The mask is a function of (seed, offset, first + element's index) alone (64-bit
+    seed and offset, taken modulo 2^64), so the same call on dy, without the
+    residual, is the backward pass. counter: an int64 device tensor of one element
+    that is added to offset when the kernel runs. y may be x or residual."""
+    dev = _device_of(x, "x")
+    types = _mx_types()
+    flat = x.dim() != 2
+    shape = x.shape
+
+    def rows_of(t, name):
+        if t.shape != shape:
+            raise ValueError(f"{name}: {tuple(t.shape)}, expected {tuple(shape)}")
+        if flat:
+            return _need_values(t, name, (x.dtype,), dev)
+        return _need_rows(t, name, (x.dtype,), dev)[2]
+
+    if flat:
+        n = _need_values(x, "x", types, dev)
+        rows, cols, x_ld = 1, n, n
+    else:
+        rows, cols, x_ld = _need_rows(x, "x", types, dev)
+    if not isinstance(y, _mx().tensor):
+        raise TypeError(f"y: a torch tensor is expected, got {type(y).__name__}")
+    y_ld = rows_of(y, "y")
+    res, res_ld = None, 0
+    if residual is not None:
+        res, res_ld = residual.data_ptr(), rows_of(residual, "residual")
+    if counter is not None:
+        counter = _vector(counter, "counter", (_torch().int64,), dev, 1)
+    mask = (1 << 64) - 1
+    _call(load().zero_dropout, dev, stream, x.data_ptr(), types[x.dtype], rows, cols, x_ld, res, res_ld, y.data_ptr(),
+          y_ld, p, seed & mask, offset & mask, counter, first)

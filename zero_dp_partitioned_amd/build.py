@@ -20,7 +20,8 @@ DEVICE = [f"--offload-arch={ARCH}", "-ffp-contract=off", "-fno-fast-math",
           "-fhip-fp32-correctly-rounded-divide-sqrt", "-fno-gpu-flush-denormals-to-zero",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 SOURCES = [("api.cpp", False), ("kernels.hip", True), ("static_scratch.hip", True), ("copy_probe.hip", True),
-           ("mx_api.cpp", False), ("mx_quant.hip", True), ("mx_product.hip", True)]
+           ("mx_api.cpp", False), ("mx_quant.hip", True), ("mx_product.hip", True),
+           ("layer_api.cpp", False), ("layer_norm.hip", True), ("dropout.hip", True)]
 
 
 def hipcc():
