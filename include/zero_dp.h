@@ -62,6 +62,14 @@ extern "C" {
 #define ZERO_DT_BF16 2 /* bfloat16 */
 #define ZERO_DT_F32 3  /* fp32 (the zero_mx_* calls and a layer's operators) */
 
+/* ---- activations of zero_gated_product (values are part of the ABI) --------
+ * sigmoid(g) = 1 / (1 + exp(-g)). */
+#define ZERO_ACT_SILU 0      /* g * sigmoid(g) */
+#define ZERO_ACT_GELU 1      /* g * (1 + erf(g / sqrt(2))) / 2 */
+#define ZERO_ACT_GELU_TANH 2 /* g * (1 + tanh(sqrt(2 / pi) * (g + 0.044715 g^3))) / 2 */
+#define ZERO_ACT_RELU 3      /* max(g, 0) */
+#define ZERO_ACT_SIGMOID 4   /* sigmoid(g) */
+
 /* ---- microscaled 4-bit format (MXFP4) ------------------------------------
  * Blocks of ZERO_MX_BLOCK consecutive values share one scale byte (E8M0:
  * 2^(byte - 127); 255 marks a NaN block), and each value is a 4-bit E2M1 code:
@@ -491,6 +499,35 @@ int zero_layer_norm_backward(const void* dy, int64_t dy_ld, const void* x, int64
 int zero_dropout(const void* x, int32_t dt, int64_t rows, int64_t cols, int64_t x_ld, const void* residual,
                  int64_t residual_ld, void* y, int64_t y_ld, double p, uint64_t seed, uint64_t offset,
                  const int64_t* counter, int64_t first, void* stream);
+
+/* The first half of a gated feed-forward block in one kernel: for x m x d and the
+ * weights w_gate and w_up f x d (of x's type, F16 or BF16, w_ld from row to row),
+ *   h = act(x w_gate^T) * (x w_up^T),   act one of ZERO_ACT_*.
+ * The products' sums are fp32 and h is formed from them before anything is
+ * rounded. gate and up (m x f, both or neither) receive the two products,
+ * rounded, for the backward pass.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (more than 2^31 - 1 rows or columns,
+ * an operand's rows more than 4,194,303 elements apart, output tiles past a
+ * launch's limit). */
+int zero_gated_product(const void* x, int32_t dt, int64_t m, int64_t d, int64_t x_ld, const void* w_gate,
+                       const void* w_up, int64_t f, int64_t w_ld, int32_t act, void* h, int64_t h_ld, void* gate,
+                       void* up, int64_t pre_ld, void* stream);
+
+/* Its backward pass, from dh (m x f) and the gate and up that the forward pass
+ * left:
+ *   dgate = dh * act'(gate) * up,   dup = dh * act(gate)   (m x f),
+ *   dx = dgate w_gate + dup w_up,   dw_gate = dgate^T x,   dw_up = dup^T x.
+ * dgate and dup are rounded to x's type, and the products are those of the rounded
+ * values (fp32 sums). They may be gate and up themselves (the same addresses and
+ * ld), which are not read again. dx may be NULL (then w_gate and w_up may be), and
+ * so may dw_gate and dw_up together (then x may be); these are of dw_dt (x's type
+ * or F32, dw_ld from row to row), and accumulate != 0 adds them to what they hold.
+ * Errors: as zero_gated_product; WORKSPACE. */
+int zero_gated_product_backward(const void* dh, int64_t dh_ld, const void* x, int32_t dt, int64_t m, int64_t d,
+                                int64_t x_ld, const void* w_gate, const void* w_up, int64_t f, int64_t w_ld, int32_t act,
+                                const void* gate, const void* up, int64_t pre_ld, void* dgate, void* dup,
+                                int64_t dpre_ld, void* dx, int64_t dx_ld, void* dw_gate, void* dw_up, int64_t dw_ld,
+                                int32_t dw_dt, int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---- testing --------------------------------------------------------------
  * Not an operation of the pages. Caps the blocks of every streaming launch

@@ -25,6 +25,7 @@ DT_F16 = 1
 DT_BF16 = 2
 DT_F32 = 3
 MX_BLOCK = 32
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 4}
 HBM_REGION_BYTES = 96 << 30
 ARENA_ALIGN = 2 << 20
 
@@ -34,7 +35,8 @@ EXPORTS = ("zero_partition", "zero_partition_tensors", "zero_workspace_bytes",
            "zero_set_grid_limit", "zero_adam_step_static", "zero_copy_probe",
            "zero_mx_cast_writeback", "zero_mx_quantize", "zero_mx_dequantize",
            "zero_mx_reduce_grad_segment", "zero_mx_product",
-           "zero_layer_norm", "zero_layer_norm_backward", "zero_dropout")
+           "zero_layer_norm", "zero_layer_norm_backward", "zero_dropout",
+           "zero_gated_product", "zero_gated_product_backward")
 
 
 class ZeroError(RuntimeError):
@@ -141,6 +143,9 @@ def load():
         L.zero_layer_norm_backward.argtypes = [vp, i64, vp, i64, i32, i64, i64, vp, i32, vp, vp, vp, i64, vp, i64, vp, vp,
                                                i32, i32, vp, sz, vp]
         L.zero_dropout.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i64, f64, u64, u64, vp, i64, vp]
+        L.zero_gated_product.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, i64, i32, vp, i64, vp, vp, i64, vp]
+        L.zero_gated_product_backward.argtypes = [vp, i64, vp, i32, i64, i64, i64, vp, vp, i64, i64, i32, vp, vp, i64, vp,
+                                                  vp, i64, vp, i64, vp, vp, i64, i32, i32, vp, sz, vp]
         for name in EXPORTS:
             fn = getattr(L, name)
             if name not in ("zero_workspace_bytes", "zero_last_error"):
@@ -899,3 +904,80 @@ def dropout(x, y, p, seed, offset=0, residual=None, first=0, counter=None, strea
     mask = (1 << 64) - 1
     _call(load().zero_dropout, dev, stream, x.data_ptr(), types[x.dtype], rows, cols, x_ld, res, res_ld, y.data_ptr(),
           y_ld, p, seed & mask, offset & mask, counter, first)
+
+
+def _activation(act):
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        raise ValueError(f"act {act!r}: expected one of {', '.join(ACTIVATIONS)}")
+    return code
+
+
+def _pair(first, second, names, dtypes, device, rows, cols):
+    """The elements from row to row of two tensors of one type, shape and row distance."""
+    ld = _like(first, names[0], dtypes, device, rows, cols)
+    if _like(second, names[1], (first.dtype,), device, rows, cols) != ld:
+        raise ValueError(f"{names[0]} and {names[1]}: rows lie {ld} and {second.stride(0)} elements apart")
+    return ld
+
+
+def _half_types():
+    return {t: c for t, c in _mx_types().items() if c != DT_F32}
+
+
+def gated_product(x, w_gate, w_up, out, act="silu", gate=None, up=None, stream=None):
+    """out = act(x w_gate^T) * (x w_up^T), the first half of a gated feed-forward
+    block, for fp16 or bf16 tensors: x [m, d], w_gate and w_up [f, d] (views of the
+    flat parameter vector serve), out [m, f]. act: silu, gelu, gelu_tanh, relu or
+    sigmoid. gate and up [m, f], both or neither, receive the two products for the
+    backward pass. w_gate and w_up have the same distance from row to row, and so
+    have gate and up."""
+    dev = _device_of(x, "x")
+    types = _half_types()
+    m, d, x_ld = _need_rows(x, "x", types, dev)
+    one = (x.dtype,)
+    f = _need_rows(w_gate, "w_gate", one, dev)[0]
+    w_ld = _pair(w_gate, w_up, ("w_gate", "w_up"), one, dev, f, d)
+    h_ld = _like(out, "out", one, dev, m, f)
+    if (gate is None) != (up is None):
+        raise ValueError("gate and up must be given together")
+    g = u = None
+    pre_ld = 0
+    if gate is not None:
+        pre_ld = _pair(gate, up, ("gate", "up"), one, dev, m, f)
+        g, u = gate.data_ptr(), up.data_ptr()
+    _call(load().zero_gated_product, dev, stream, x.data_ptr(), types[x.dtype], m, d, x_ld, w_gate.data_ptr(),
+          w_up.data_ptr(), f, w_ld, _activation(act), out.data_ptr(), h_ld, g, u, pre_ld)
+
+
+def gated_product_backward(dout, x, w_gate, w_up, gate, up, dgate, dup, workspace, dx=None, dw_gate=None, dw_up=None,
+                           act="silu", accumulate=False, stream=None):
+    """The gradients of gated_product from dout [m, f] and the gate and up it left:
+    dgate and dup [m, f] (which may be gate and up themselves: they are not needed
+    again), from these dx = dgate w_gate + dup w_up [m, d], and dw_gate = dgate^T x
+    and dw_up = dup^T x [f, d], of x's type or fp32, added to what they hold with
+    `accumulate`. dx, and dw_gate with dw_up, may be None. Views into a flat
+    gradient copy serve for dw_gate and dw_up."""
+    dev = _device_of(x, "x")
+    types = _half_types()
+    m, d, x_ld = _need_rows(x, "x", types, dev)
+    one = (x.dtype,)
+    f = _need_rows(w_gate, "w_gate", one, dev)[0]
+    w_ld = _pair(w_gate, w_up, ("w_gate", "w_up"), one, dev, f, d)
+    dh_ld = _like(dout, "dout", one, dev, m, f)
+    pre_ld = _pair(gate, up, ("gate", "up"), one, dev, m, f)
+    dpre_ld = _pair(dgate, dup, ("dgate", "dup"), one, dev, m, f)
+    ws, ws_bytes = _scratch(workspace, dev)
+    dx_p, dx_ld = None, 0
+    if dx is not None:
+        dx_p, dx_ld = dx.data_ptr(), _like(dx, "dx", one, dev, m, d)
+    if (dw_gate is None) != (dw_up is None):
+        raise ValueError("dw_gate and dw_up must be given together")
+    dg = du = None
+    dw_ld = dw_dt = 0
+    if dw_gate is not None:
+        dw_ld = _pair(dw_gate, dw_up, ("dw_gate", "dw_up"), (x.dtype, _mx().f32), dev, f, d)
+        dg, du, dw_dt = dw_gate.data_ptr(), dw_up.data_ptr(), _mx_types()[dw_gate.dtype]
+    _call(load().zero_gated_product_backward, dev, stream, dout.data_ptr(), dh_ld, x.data_ptr(), types[x.dtype], m, d,
+          x_ld, w_gate.data_ptr(), w_up.data_ptr(), f, w_ld, _activation(act), gate.data_ptr(), up.data_ptr(), pre_ld,
+          dgate.data_ptr(), dup.data_ptr(), dpre_ld, dx_p, dx_ld, dg, du, dw_ld, dw_dt, bool(accumulate), ws, ws_bytes)

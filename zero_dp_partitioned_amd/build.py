@@ -7,6 +7,7 @@ instructions disabled.
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -15,13 +16,15 @@ LIB = os.path.join(HERE, "libzero_dp.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 
 ARCH = "gfx950"
+JOBS = 6  # files compiled at a time
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-I", os.path.join(ROOT, "include")]
 DEVICE = [f"--offload-arch={ARCH}", "-ffp-contract=off", "-fno-fast-math",
           "-fhip-fp32-correctly-rounded-divide-sqrt", "-fno-gpu-flush-denormals-to-zero",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 SOURCES = [("api.cpp", False), ("kernels.hip", True), ("static_scratch.hip", True), ("copy_probe.hip", True),
            ("mx_api.cpp", False), ("mx_quant.hip", True), ("mx_product.hip", True),
-           ("layer_api.cpp", False), ("layer_norm.hip", True), ("dropout.hip", True)]
+           ("layer_api.cpp", False), ("layer_norm.hip", True), ("dropout.hip", True),
+           ("gated_product.hip", True)]
 
 
 def hipcc():
@@ -33,8 +36,8 @@ def hipcc():
 
 def build(verbose=False, extra_device_flags=()):
     os.makedirs(BUILD_DIR, exist_ok=True)
-    objs = []
-    for name, device in SOURCES:
+
+    def compile_one(name, device):
         src = os.path.join(CSRC, name)
         obj = os.path.join(BUILD_DIR, name + ".o")
         if device:
@@ -45,7 +48,10 @@ def build(verbose=False, extra_device_flags=()):
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
-        objs.append(obj)
+        return obj
+
+    with ThreadPoolExecutor(JOBS) as pool:
+        objs = list(pool.map(lambda source: compile_one(*source), SOURCES))
     tmp = LIB + ".tmp"
     cmd = [hipcc(), "-shared", f"--offload-arch={ARCH}", *objs, "-o", tmp]
     if verbose:

@@ -1,0 +1,752 @@
+// gfx950 kernels of a gated feed-forward block's first half and its gradients,
+//   g = x wg^T,  u = x wu^T,  h = act(g) * u,
+//   dg = dh act'(g) u,  du = dh act(g),
+//   dx = dg wg + du wu,  dwg = dg^T x,  dwu = du^T x,
+// in fp16 or bf16 on v_mfma_f32_32x32x16 (fp32 sums). The products are three
+// uses of one tile kernel, which differ in how their operands lie in memory:
+//   forward  A = x, B = wg and wu side by side: contraction along the rows of both;
+//   dx       A = dg then du, along its rows; B = wg then wu, along its columns;
+//   dw       A = dg or du, B = x, along the columns of both.
+// Operands reach LDS as they lie. An operand along the rows is read back 16
+// bytes a lane; one along the columns through ds_read_b64_tr_b16, which
+// transposes 4 x 16 values on the way, so no transposed copy is ever made.
+#include <atomic>
+#include <type_traits>
+
+#include "layer_device.h"
+
+namespace zdp {
+namespace {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef short s8 __attribute__((ext_vector_type(8)));
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+
+enum Use { kForward, kDx, kDw };
+
+// How operands reach LDS: kDirect by fetches that write it themselves (every
+// 16-byte slot of the operands aligned and whole), kStaged through registers
+// (aligned to elements), kMasked value by value (a dimension smaller than the tile).
+enum Fetch { kDirect, kStaged, kMasked };
+
+constexpr int kFrag = 32;      // rows of an operand per instruction
+constexpr int kChunk = 64;     // contraction per stage: 128 bytes of a row
+constexpr int kSteps = 4;      // of 16, per chunk
+constexpr int kPiece = 1024;   // bytes that a wave moves at a time
+constexpr int kPieceRows = 8;  // rows, or as much of the contraction as a piece's columns leave, of a piece
+
+struct ProductArgs {
+  const char* a[2];
+  const char* b[2];
+  int64_t a_ld, b_ld;  // bytes from row to row
+  int64_t m, n, k;     // rows and columns of an output; contraction (of one of dx's two parts)
+  void* out[3];
+  int64_t out_ld[3];
+  int32_t act, accumulate;
+  int32_t splits;  // blocks that share a tile's contraction, each leaving fp32 sums at `partial`
+  float* partial;  // [splits][outputs][m][n]
+};
+
+// ------------------------------------------------------------------------
+// The activation and its derivative. exp and 1 / x are the hardware's: within
+// (|x| + 4) 2^-24 of themselves, far inside the 16-bit results' rounding.
+// ------------------------------------------------------------------------
+
+__device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + __expf(-x)); }
+
+constexpr float kTanhA = 1.5957691216057308f;   // 2 sqrt(2 / pi)
+constexpr float kTanhB = 0.044715f;
+
+__device__ __forceinline__ float activation(float g, int32_t act) {
+  switch (act) {
+    case ZERO_ACT_SILU: return g * sigmoid(g);
+    case ZERO_ACT_GELU: return 0.5f * g * erfcf(-0.70710678118654752f * g);
+    case ZERO_ACT_GELU_TANH: return g * sigmoid(kTanhA * g * __builtin_fmaf(kTanhB * g, g, 1.f));
+    case ZERO_ACT_RELU: return g <= 0.f ? 0.f : g;  // NaN stays
+    default: return sigmoid(g);
+  }
+}
+
+__device__ __forceinline__ void activation_grad(float g, int32_t act, float* a, float* da) {
+  switch (act) {
+    case ZERO_ACT_SILU: {
+      const float s = sigmoid(g), r = sigmoid(-g);
+      *a = g * s;
+      *da = __builtin_fmaf(*a, r, s);
+      return;
+    }
+    case ZERO_ACT_GELU: {
+      const float c = 0.5f * erfcf(-0.70710678118654752f * g);
+      *a = g * c;
+      *da = __builtin_fmaf(0.3989422804014327f * g, __expf(-0.5f * g * g), c);
+      return;
+    }
+    case ZERO_ACT_GELU_TANH: {
+      const float z = kTanhA * g * __builtin_fmaf(kTanhB * g, g, 1.f), s = sigmoid(z), r = sigmoid(-z);
+      *a = g * s;
+      *da = __builtin_fmaf(*a * r, kTanhA * __builtin_fmaf(3.f * kTanhB * g, g, 1.f), s);
+      return;
+    }
+    case ZERO_ACT_RELU:
+      *a = g <= 0.f ? 0.f : g;
+      *da = g <= 0.f ? 0.f : 1.f;
+      return;
+    default: {
+      const float s = sigmoid(g);
+      *a = s;
+      *da = s * sigmoid(-g);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------
+// Pieces of the tile kernel
+// ------------------------------------------------------------------------
+
+template <int DT>
+__device__ __forceinline__ v16f mfma(s8 b, s8 a, v16f c) {
+  if constexpr (DT == ZERO_DT_BF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, b), __builtin_bit_cast(b8, a), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, b), __builtin_bit_cast(h8, a), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ s8 read16(uint32_t lds) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) s8*>(lds);
+}
+
+__device__ __forceinline__ s4 read_tr(uint32_t lds) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<__attribute__((address_space(3))) s4*>(lds));
+}
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)p));
+}
+
+// m0 is named as overwritten, so that the compiler keeps no value of its own
+// there across a fetch. It warns about every such list because it reserves m0
+// and cannot save it; nothing needs it saved.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+
+// If i < n (uniform): fetch 16 bytes a lane from base + off into LDS at `lds` +
+// 16 * lane. No vector register is written; the caller waits on vmcnt. The
+// branch is the asm's own, as one that the compiler sees would split the loop
+// around it; compare and branch are the wait state that the hardware wants
+// between the write of m0 and the load that takes its LDS base from it.
+__device__ __forceinline__ void fetch_to_lds_if(uint32_t i, uint32_t n, const char* base, uint32_t off, uint32_t lds) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\ts_cmp_ge_u32 %3, %4\n\ts_cbranch_scc1 .Lzdp_skip%=\n\t"
+      "global_load_lds_dwordx4 %1, %2\n.Lzdp_skip%=:" ::"s"(lds), "v"(off), "s"(base), "s"(i), "s"(n)
+      : "memory", "scc", "m0");
+}
+
+#pragma clang diagnostic pop
+
+// Tiles dealt to the eight XCDs (block b runs on XCD b % 8) in contiguous
+// runs, and inside a run in columns of kGroup tile rows, so that the tiles that
+// an XCD's 32 CUs work on at a time share their operands in its L2.
+constexpr int kXcds = 8;
+constexpr int kGroup = 8;
+
+__device__ __forceinline__ void tile_of(uint32_t b, uint32_t tm, uint32_t tn, uint32_t* m, uint32_t* n) {
+  const uint32_t total = tm * tn, q = total / kXcds, rem = total % kXcds;
+  const uint32_t x = b % kXcds;
+  const uint32_t i = x * q + (x < rem ? x : rem) + b / kXcds;
+  const uint32_t width = kGroup * tn, first = i / width * kGroup;
+  const uint32_t rows = tm - first < kGroup ? tm - first : kGroup;
+  const uint32_t at = i % width;
+  *m = __builtin_amdgcn_readfirstlane(first + at % rows);
+  *n = __builtin_amdgcn_readfirstlane(at / rows);
+}
+
+// An operand of SIZE rows (or columns) in LDS, kChunk of the contraction.
+//
+// Along the rows: rows of 128 bytes, eight slots of 16; slot b of row i stands
+// at b ^ (i / 2) % 8, so that one slot of 16 neighbouring rows lies in 16
+// different groups of four of the 64 banks.
+//
+// Along the columns: SIZE columns side by side, kChunk lines of them. A
+// transposing read takes 8 bytes a lane, four lines of 32 bytes for 16 lanes;
+// slot b of line k stands at b ^ mix(k), so that the lines which are read
+// together lie in different banks.
+template <int SIZE, bool COLS>
+struct Operand {
+  static constexpr int kBytes = SIZE * kChunk * 2;
+  static constexpr int kSlots = COLS ? SIZE / 8 : 8;  // of a line
+  static constexpr int kLine = kSlots * 16;
+  static constexpr int kPieceLines = kPiece / kLine;
+
+  static __device__ __forceinline__ int mix(int line) {
+    if constexpr (!COLS) return line >> 1 & 7;
+    else if constexpr (kSlots >= 16) return (line & 3) << 2 | (line >> 3 & 1) << 1;
+    else return (line >> 1 & 1) << 2 | (line >> 3 & 1) << 1;
+  }
+  // The line and slot (of 8 values) that lane `lane` of piece p moves.
+  static __device__ __forceinline__ int line(int p, int lane) { return p * kPieceLines + lane / kSlots; }
+  static __device__ __forceinline__ int slot(int p, int lane) { return (lane % kSlots) ^ mix(line(p, lane)); }
+
+  // Where a lane reads fragment rows (columns) first .. first + 31 of step 0;
+  // `first` is a multiple of 32.
+  static __device__ __forceinline__ uint32_t fragment(int first, int lane) {
+    if constexpr (!COLS) {
+      return (first + (lane & 31)) * kLine + ((lane >> 5) ^ mix(lane & 31)) * 16;
+    } else {
+      const int k = 8 * (lane >> 5) + (lane >> 2 & 3);
+      return k * kLine + ((first / 8 + 2 * (lane >> 4 & 1) + (lane >> 1 & 1)) ^ mix(k)) * 16 + (lane & 1) * 8;
+    }
+  }
+  static __device__ __forceinline__ s8 read(uint32_t at, int step) {
+    if constexpr (!COLS) {
+      return read16(at ^ (step * 32));  // slots 2 * step + ...: the mix is an exclusive or
+    } else {
+      const s4 lo = read_tr(at + step * 16 * kLine), hi = read_tr(at + (step * 16 + 4) * kLine);
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+  }
+};
+
+// ------------------------------------------------------------------------
+// The tile kernel: WM x WN waves, each with FM x FN fragments, share an output
+// tile through LDS, two stages of one chunk each. A stage is fetched while the
+// stage before is multiplied, the loads between the products. The rows of B of
+// a forward tile are, wave column by wave column, FN / 2 fragments of wg and the
+// same of wu, so that a lane holds g and u of the same outputs.
+// ------------------------------------------------------------------------
+
+template <Use USE, int FM, int FN, int WM, int WN>
+struct Tile {
+  static constexpr int kM = kFrag * FM * WM, kN = kFrag * FN * WN;
+  static constexpr int kOutN = USE == kForward ? kN / 2 : kN;  // columns of an output
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  using A = Operand<kM, USE == kDw>;
+  using B = Operand<kN, USE != kForward>;
+  static constexpr int kPiecesA = A::kBytes / kPiece, kPiecesB = B::kBytes / kPiece;
+  static constexpr int kLoadsA = kPiecesA / kWaves, kLoads = (kPiecesA + kPiecesB) / kWaves;
+  static constexpr int kStage = A::kBytes + B::kBytes;
+  static constexpr int kRunN = kOutN / WN;  // columns of a wave's output
+  static constexpr int kOutRow = kRunN + 4;  // floats, padded
+  static constexpr int kOut = kWaves * kFrag * kOutRow * 4;
+  static constexpr int kLds = 2 * kStage > kOut ? 2 * kStage : kOut;
+  static_assert(kLds <= 160 * 1024, "LDS of a CU");
+  static_assert(kPiecesA % kWaves == 0 && kPiecesB % kWaves == 0, "a load's pieces belong to one operand");
+};
+
+__device__ __forceinline__ uint32_t tiles_of(int64_t n, uint32_t size) { return static_cast<uint32_t>((n + size - 1) / size); }
+
+// Registers: two waves a SIMD (256 each) for the largest tile, of which one
+// block fills a CU; more blocks of the smaller ones.
+template <Use USE, Fetch FETCH, int FM, int FN, int WM, int WN, int DT, int ODT>
+__global__ void __launch_bounds__(64 * WM * WN, 2) gated_tile_kernel(const ProductArgs P) {
+  using T = Tile<USE, FM, FN, WM, WN>;
+  using A = typename T::A;
+  using B = typename T::B;
+  extern __shared__ __align__(1024) uint8_t lds[];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t tiles_m = tiles_of(P.m, T::kM), tiles_n = tiles_of(P.n, T::kOutN);
+  const uint32_t rows = USE == kDw ? 2 * tiles_m : tiles_m;  // dwu's tiles behind dwg's
+  const uint32_t split = P.splits > 1 ? blockIdx.x / (rows * tiles_n) : 0;
+  uint32_t tm, tn;
+  tile_of(P.splits > 1 ? blockIdx.x % (rows * tiles_n) : blockIdx.x, rows, tiles_n, &tm, &tn);
+  const int z = USE == kDw && tm >= tiles_m;  // which output
+  if (z) tm -= tiles_m;
+  // The tile's first row and column, and the first of the operands': along the
+  // columns the last tile is moved back to end with the operand, so that every
+  // load is whole; what the tile before has is not written again.
+  const int64_t m0 = static_cast<int64_t>(tm) * T::kM, n0 = static_cast<int64_t>(tn) * T::kOutN;
+  int64_t am0 = m0, bn0 = n0;
+  if (FETCH != kMasked) {
+    if (USE == kDw && am0 > P.m - T::kM) am0 = P.m - T::kM;
+    if (USE != kForward && bn0 > P.n - T::kN) bn0 = P.n - T::kN;
+  }
+
+  // The contraction: `parts` runs of `whole` chunks, of which this block takes
+  // [c0, c0 + stages); what is left of a run behind its last whole chunk goes
+  // first, to split 0.
+  constexpr int kParts = USE == kDx ? 2 : 1;
+  const uint32_t rest = FETCH == kMasked ? 0 : static_cast<uint32_t>(P.k % kChunk);
+  const uint32_t whole = static_cast<uint32_t>(FETCH == kMasked ? (P.k + kChunk - 1) / kChunk : P.k / kChunk);
+  const uint32_t all = kParts * whole;
+  const uint32_t c0 = P.splits > 1 ? static_cast<uint32_t>(static_cast<uint64_t>(all) * split / P.splits) : 0;
+  const uint32_t c1 = P.splits > 1 ? static_cast<uint32_t>(static_cast<uint64_t>(all) * (split + 1) / P.splits) : all;
+  const uint32_t stages = c1 - c0;
+
+  // Load j of a wave: a piece of A (j < kLoadsA) or B. Where its lanes start,
+  // from the operand's first row (column) of the tile.
+  uint32_t off[T::kLoads];
+  // (scalars: selects over an array become an array in scratch memory)
+  const int64_t atile = USE == kDw ? am0 * 2 : m0 * P.a_ld, btile = USE == kForward ? n0 * P.b_ld : bn0 * 2;
+  const char* const a0 = (z ? P.a[1] : P.a[0]) + atile;
+  const char* const a1 = USE == kDx ? P.a[1] + atile : a0;
+  const char* const b0 = P.b[0] + btile;
+  const char* const b1 = USE == kDw ? b0 : P.b[1] + btile;
+  const int64_t astep = USE == kDw ? kChunk * P.a_ld : kChunk * 2, bstep = USE == kForward ? kChunk * 2 : kChunk * P.b_ld;
+  auto piece = [&](int j) { return j < T::kLoadsA ? j * T::kWaves + w : (j - T::kLoadsA) * T::kWaves + w; };
+  // Row of B's operand in wg or wu that LDS row `row` holds, and which of them.
+  constexpr int kHalf = kFrag * FN / 2;
+  auto weight_row = [&](int row) { return row / (2 * kHalf) * kHalf + row % kHalf; };
+  auto weight_of = [&](int row) { return row / kHalf & 1; };
+#pragma unroll
+  for (int j = 0; j < T::kLoads; ++j) {
+    const bool is_a = j < T::kLoadsA;
+    const int line = is_a ? A::line(piece(j), lane) : B::line(piece(j), lane);
+    const int slot = is_a ? A::slot(piece(j), lane) : B::slot(piece(j), lane);
+    int64_t row = line;  // rows past the end repeat the last one
+    if (is_a && USE != kDw) row = row < P.m - 1 - m0 ? row : P.m - 1 - m0;
+    if (!is_a && USE == kForward) {
+      row = weight_row(line);
+      row = row < P.n - 1 - n0 ? row : P.n - 1 - n0;
+    }
+    off[j] = static_cast<uint32_t>(row * (is_a ? P.a_ld : P.b_ld) + slot * 16);
+  }
+  // Where load j of chunk c starts.
+  auto from = [&](uint32_t c, int j) -> const char* {
+    const int part = kParts == 2 && c >= whole;
+    const uint64_t at = part ? c - whole : c;
+    if (j < T::kLoadsA) return (part ? a1 : a0) + at * astep;
+    return ((USE == kForward ? weight_of(piece(j) * kPieceRows) : part) ? b1 : b0) + at * bstep;
+  };
+  // The lane's 16 bytes of load j of a chunk that is not whole, or of an operand
+  // smaller than the tile: what does not exist is zero.
+  auto masked = [&](int part, uint32_t at, int j) -> u4 {
+    const bool is_a = j < T::kLoadsA, cols = is_a ? USE == kDw : USE != kForward;
+    const int line = is_a ? A::line(piece(j), lane) : B::line(piece(j), lane);
+    const int slot = is_a ? A::slot(piece(j), lane) : B::slot(piece(j), lane);
+    const char* base = is_a ? (part ? a1 : a0) : ((USE == kForward ? weight_of(piece(j) * kPieceRows) : part) ? b1 : b0);
+    base += static_cast<uint64_t>(at) * (is_a ? astep : bstep) + off[j];
+    const int64_t k0 = static_cast<int64_t>(at) * kChunk;
+    int64_t left;
+    if (cols) left = k0 + line < P.k ? (is_a ? P.m - am0 : P.n - bn0) - slot * 8 : 0;
+    else left = P.k - k0 - slot * 8;
+    u4 x = {0, 0, 0, 0};
+    if (left > 0) x = load_part<DT>(base, left);
+    return x;
+  };
+  auto put = [&](int buffer, int j, u4 x) {
+    *reinterpret_cast<u4*>(lds + buffer * T::kStage + (j < T::kLoadsA ? 0 : A::kBytes) + piece(j) * kPiece + lane * 16) = x;
+  };
+
+  const int wm = w / WN, wn = w % WN;
+  const uint32_t lds0 = lds_address(lds);
+  uint32_t aat[FM], bat[FN];
+#pragma unroll
+  for (int f = 0; f < FM; ++f) aat[f] = lds0 + A::fragment((wm * FM + f) * kFrag, lane);
+#pragma unroll
+  for (int f = 0; f < FN; ++f) bat[f] = lds0 + A::kBytes + B::fragment((wn * FN + f) * kFrag, lane);
+  s8 a[2][FM], b[2][FN];
+  // Fragment f of step s of the stage in `buffer`: B's first two, A's first, then
+  // the rest, in the order in which the products need them.
+  auto read = [&](uint32_t buffer, int s, int f) {
+    const uint32_t at = buffer * T::kStage;
+    if (f < 2) b[s & 1][f] = B::read(bat[f] + at, s);
+    else if (f == 2) a[s & 1][0] = A::read(aat[0] + at, s);
+    else if (f <= FN) b[s & 1][f - 1] = B::read(bat[f - 1] + at, s);
+    else a[s & 1][f - FN] = A::read(aat[f - FN] + at, s);
+  };
+  v16f acc[FM][FN] = {};
+
+  // What is left behind the whole chunks, one run after the other.
+  if (FETCH != kMasked && rest && split == 0) {
+#pragma unroll 1
+    for (int part = 0; part < kParts; ++part) {
+      u4 x[T::kLoads];
+#pragma unroll
+      for (int j = 0; j < T::kLoads; ++j) x[j] = masked(part, whole, j);
+      if (part) __syncthreads();  // read out
+#pragma unroll
+      for (int j = 0; j < T::kLoads; ++j) put(1, j, x[j]);
+      __syncthreads();
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+#pragma unroll
+        for (int f = 0; f < FM + FN; ++f) read(1, s, f);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) acc[i][j] = mfma<DT>(b[s & 1][j], a[s & 1][i], acc[i][j]);
+      }
+    }
+    __syncthreads();
+  }
+
+  if (stages) {
+    u4 pend[FETCH == kDirect ? 1 : T::kLoads];
+    // Load j of stage i: into LDS if there is that stage, or (the last stage
+    // again past the end) into registers.
+    auto fetch = [&](uint32_t i, int j) {
+      if constexpr (FETCH == kDirect) {
+        const uint32_t c = c0 + i;
+        fetch_to_lds_if(i, stages, from(c, j), off[j],
+                        lds0 + (i & 1) * T::kStage + (j < T::kLoadsA ? 0 : A::kBytes) + piece(j) * kPiece);
+      } else {
+        const uint32_t c = c0 + (i < stages ? i : stages - 1);
+        if constexpr (FETCH == kStaged) pend[j] = load_any(from(c, j) + off[j]);
+        else pend[j] = masked(kParts == 2 && c >= whole, kParts == 2 && c >= whole ? c - whole : c, j);
+      }
+    };
+    // Stage i, fetched, to every wave. All of them have read out its buffer's stage before.
+    auto publish = [&](uint32_t i) {
+      if constexpr (FETCH == kDirect) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      } else {
+#pragma unroll
+        for (int j = 0; j < T::kLoads; ++j) put(i & 1, j, pend[j]);
+      }
+      __syncthreads();
+    };
+    constexpr int kPer = FM * FN >= 4 ? 2 : 1;          // products of a group
+    constexpr int kGroups = FM * FN / kPer;             // per step
+    constexpr int kReads = (FM + FN + kGroups - 1) / kGroups;            // per group
+    constexpr int kLateReads = (FM + FN + kGroups - 2) / (kGroups - 1);  // per group of the last step but its first
+    constexpr int kFetches = (T::kLoads + 2 * kGroups) / (2 * kGroups + 1);
+    // One step: per group its products and a few reads of the next step's
+    // fragments, the order fixed so that reads and products leave in turn. The
+    // last step publishes the next stage behind its first group (every wave has
+    // read this stage out by then) and starts fetching the one after it into
+    // this stage's place; the next stage's first steps fetch the rest. Stages
+    // that pass through registers are fetched in their predecessor's first steps.
+    auto step = [&](auto sc, uint32_t i) {
+      constexpr int S = decltype(sc)::value;
+#pragma unroll
+      for (int t = 0; t < kGroups; ++t) {
+        if constexpr (S == kSteps - 1) {
+          if (t == 1) publish(i + 1);
+        }
+        if constexpr (FETCH == kDirect) {
+          const int slot = S == kSteps - 1 ? t - 1 : kGroups - 1 + S * kGroups + t;
+#pragma unroll
+          for (int q = 0; q < kFetches; ++q)
+            if (slot >= 0 && slot * kFetches + q < T::kLoads) fetch(i + (S == kSteps - 1 ? 2 : 1), slot * kFetches + q);
+        } else if constexpr (S < 2) {
+          constexpr int kEach = (T::kLoads + 2 * kGroups - 1) / (2 * kGroups);
+#pragma unroll
+          for (int q = 0; q < kEach; ++q)
+            if ((S * kGroups + t) * kEach + q < T::kLoads) fetch(i + 1, (S * kGroups + t) * kEach + q);
+        }
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+          const int x = (t * kPer + q) / FN, y = (t * kPer + q) % FN;
+          acc[x][y] = mfma<DT>(b[S & 1][y], a[S & 1][x], acc[x][y]);
+        }
+        if constexpr (S < kSteps - 1) {
+#pragma unroll
+          for (int q = 0; q < kReads; ++q)
+            if (t * kReads + q < FM + FN) read(i & 1, S + 1, t * kReads + q);
+        } else if (t > 0) {
+#pragma unroll
+          for (int q = 0; q < kLateReads; ++q)
+            if ((t - 1) * kLateReads + q < FM + FN) read((i + 1) & 1, 0, (t - 1) * kLateReads + q);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+#pragma unroll
+    for (int j = 0; j < T::kLoads; ++j) fetch(0, j);
+    publish(0);
+#pragma unroll
+    for (int f = 0; f < FM + FN; ++f) read(0, 0, f);
+    if constexpr (FETCH == kDirect) {
+      constexpr int kEarly = (kGroups - 1) * kFetches < T::kLoads ? (kGroups - 1) * kFetches : T::kLoads;
+#pragma unroll
+      for (int j = 0; j < kEarly; ++j) fetch(1, j);
+    }
+    uint32_t i = 0;
+    do {
+      step(std::integral_constant<int, 0>{}, i);
+      step(std::integral_constant<int, 1>{}, i);
+      step(std::integral_constant<int, 2>{}, i);
+      step(std::integral_constant<int, 3>{}, i);
+    } while (++i < stages);
+    __syncthreads();
+  }
+
+  // 32 rows of the wave's part of the tile at a time, through LDS, so that a row
+  // leaves in runs of 16 bytes a lane. A lane holds columns 8 q + 4 (lane / 32) +
+  // 0..3 of row lane % 32 of a fragment.
+  float* const mine = reinterpret_cast<float*>(lds) + w * kFrag * T::kOutRow;
+  const int r = lane & 31, half = lane >> 5;
+  auto rows_out = [&](auto type, int i, void* out, int64_t ld, bool add, auto&& value) {
+    constexpr int O = decltype(type)::value, kVals = Vec<O>::kVals, kElem = Vec<O>::kElem;
+    constexpr int kFrags = T::kRunN / kFrag;
+#pragma unroll
+    for (int j = 0; j < kFrags; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        f4 x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = value(j, 4 * q + e);
+        *reinterpret_cast<f4*>(mine + r * T::kOutRow + j * kFrag + 8 * q + 4 * half) = x;
+      }
+    __builtin_amdgcn_wave_barrier();
+    constexpr int kRuns = T::kRunN / kVals;  // of a row
+#pragma unroll
+    for (int t = 0; t < kFrag * kRuns / 64; ++t) {
+      const int row = (t * 64 + lane) / kRuns, col = (t * 64 + lane) % kRuns * kVals;
+      float v[kVals];
+#pragma unroll
+      for (int q = 0; q < kVals / 4; ++q) {
+        const f4 x = *reinterpret_cast<const f4*>(mine + row * T::kOutRow + col + 4 * q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * q + e] = x[e];
+      }
+      const int64_t om = am0 + (wm * FM + i) * kFrag + row, on = bn0 + wn * T::kRunN + col;
+      if (om < m0 || om >= P.m || on >= P.n || on + kVals <= n0) continue;
+      char* const to = static_cast<char*>(out) + (om * ld + on) * kElem;
+      const int first = on < n0 ? static_cast<int>(n0 - on) : 0;
+      const int end = P.n - on < kVals ? static_cast<int>(P.n - on) : kVals;
+      if (first == 0 && end == kVals) {
+        if (add) {
+          float old[kVals];
+          widen<O>(load_any(to), old);
+#pragma unroll
+          for (int e = 0; e < kVals; ++e) v[e] += old[e];
+        }
+        const u4 x = narrow<O>(v);
+        __builtin_memcpy(to, &x, 16);
+      } else {
+        if (add) {
+#pragma unroll
+          for (int e = 0; e < kVals; ++e)
+            if (e >= first && e < end) v[e] += load_one(to, e, O);
+        }
+        store_some<O>(to, first, end, narrow<O>(v));
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  };
+  using Type = std::integral_constant<int, ODT>;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    if constexpr (USE == kForward) {
+      constexpr int H = FN / 2;
+      rows_out(Type{}, i, P.out[0], P.out_ld[0], false,
+               [&](int j, int e) { return activation(acc[i][j][e], P.act) * acc[i][j + H][e]; });
+      if (P.out[1]) {
+        rows_out(Type{}, i, P.out[1], P.out_ld[1], false, [&](int j, int e) { return acc[i][j][e]; });
+        rows_out(Type{}, i, P.out[2], P.out_ld[2], false, [&](int j, int e) { return acc[i][j + H][e]; });
+      }
+    } else if (P.splits > 1) {
+      float* const to = P.partial + (static_cast<int64_t>(split) * (USE == kDw ? 2 : 1) + z) * P.m * P.n;
+      rows_out(std::integral_constant<int, ZERO_DT_F32>{}, i, to, P.n, false, [&](int j, int e) { return acc[i][j][e]; });
+    } else {
+      rows_out(Type{}, i, P.out[z], P.out_ld[z], P.accumulate, [&](int j, int e) { return acc[i][j][e]; });
+    }
+  }
+}
+
+// The splits' sums, added in order. Two rows of `n` values a row of the grid's y
+// for a pair of outputs.
+template <int ODT>
+__global__ void __launch_bounds__(256) gated_join_kernel(const ProductArgs P, int outputs) {
+  const int64_t each = P.m * P.n;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < each; i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int z = blockIdx.y;
+    float s = 0.f;
+    for (int q = 0; q < P.splits; ++q) s += P.partial[(static_cast<int64_t>(q) * outputs + z) * each + i];
+    const int64_t row = i / P.n, at = row * P.out_ld[z] + (i - row * P.n);
+    if (P.accumulate) s += load_one(P.out[z], at, ODT);
+    store_one(P.out[z], at, ODT, s);
+  }
+}
+
+// ------------------------------------------------------------------------
+// dg = dh act'(g) u, du = dh act(g): a streaming pass. dg and du may lie where g and u do.
+// ------------------------------------------------------------------------
+
+struct GateGradArgs {
+  Rows dh, pre[2];
+  RowsOut dpre[2];
+  int64_t rows, cols;
+  int32_t act;
+};
+
+template <int DT>
+__global__ void __launch_bounds__(256) gate_grad_kernel(const GateGradArgs G, int64_t row_slots, int64_t slots) {
+  constexpr int kVals = Vec<DT>::kVals;
+  for (int64_t s = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; s < slots; s += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t row = G.rows > 1 ? s / row_slots : 0, col = (s - row * row_slots) * kVals, left = G.cols - col;
+    float dh[kVals], g[kVals], u[kVals];
+    widen<DT>(load_part<DT>(static_cast<const char*>(G.dh.p) + (row * G.dh.ld + col) * 2, left), dh);
+    widen<DT>(load_part<DT>(static_cast<const char*>(G.pre[0].p) + (row * G.pre[0].ld + col) * 2, left), g);
+    widen<DT>(load_part<DT>(static_cast<const char*>(G.pre[1].p) + (row * G.pre[1].ld + col) * 2, left), u);
+#pragma unroll
+    for (int e = 0; e < kVals; ++e) {
+      float a, da;
+      activation_grad(g[e], G.act, &a, &da);
+      g[e] = dh[e] * da * u[e];
+      u[e] = dh[e] * a;
+    }
+    store_part<DT>(static_cast<char*>(G.dpre[0].p) + (row * G.dpre[0].ld + col) * 2, left, narrow<DT>(g));
+    store_part<DT>(static_cast<char*>(G.dpre[1].p) + (row * G.dpre[1].ld + col) * 2, left, narrow<DT>(u));
+  }
+}
+
+// ------------------------------------------------------------------------
+// Launches
+// ------------------------------------------------------------------------
+
+template <Use USE, Fetch FETCH, int FM, int FN, int WM, int WN, int DT, int ODT>
+hipError_t tile_launch(const ProductArgs& a, hipStream_t s) {
+  using T = Tile<USE, FM, FN, WM, WN>;
+  const auto kernel = gated_tile_kernel<USE, FETCH, FM, FN, WM, WN, DT, ODT>;
+  const int64_t tiles = ceil_div(a.m, T::kM) * ceil_div(a.n, T::kOutN) * (USE == kDw ? 2 : 1);
+  if (tiles > INT32_MAX / T::kThreads / (a.splits > 1 ? a.splits : 1)) return hipErrorInvalidConfiguration;
+  // more than the default limit of 64 KiB of dynamic LDS, granted once per kernel and device
+  static std::atomic<uint64_t> granted{0};
+  int dev = 0;
+  if (hipError_t e = hipGetDevice(&dev)) return e;
+  const uint64_t bit = uint64_t{1} << (dev & 63);
+  if (dev > 63 || !(granted.load(std::memory_order_acquire) & bit)) {
+    if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds))
+      return e;
+    granted.fetch_or(bit, std::memory_order_release);
+  }
+  const int64_t blocks = tiles * (a.splits > 1 ? a.splits : 1);
+  hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(blocks)), dim3(T::kThreads), T::kLds, s, a);
+  return hipGetLastError();
+}
+
+bool aligned16(const void* p, int64_t ld_bytes) { return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld_bytes)) & 15) == 0; }
+
+constexpr int64_t kEnoughTiles = 160;
+
+// One tile shape with the fetch that the operands allow.
+template <Use USE, int FM, int FN, int WM, int WN, int DT, int ODT>
+hipError_t fetch_launch(const ProductArgs& a, hipStream_t s) {
+  using T = Tile<USE, FM, FN, WM, WN>;
+  if constexpr (FM == 1 && USE != kForward) {
+    if ((USE == kDw && a.m < T::kM) || a.n < T::kN) return tile_launch<USE, kMasked, FM, FN, WM, WN, DT, ODT>(a, s);
+  }
+  // a moved tile starts at n - kN: on 16 bytes if n is
+  bool direct = aligned16(a.a[0], a.a_ld) && aligned16(a.b[0], a.b_ld) && (!a.a[1] || aligned16(a.a[1], a.a_ld)) &&
+                (!a.b[1] || aligned16(a.b[1], a.b_ld));
+  if (USE == kDw) direct = direct && a.m % 8 == 0;
+  if (USE != kForward) direct = direct && a.n % 8 == 0;
+  if (direct) return tile_launch<USE, kDirect, FM, FN, WM, WN, DT, ODT>(a, s);
+  return tile_launch<USE, kStaged, FM, FN, WM, WN, DT, ODT>(a, s);
+}
+
+template <Use USE, int DT, int ODT>
+hipError_t product_launch(ProductArgs a, float* scratch, hipStream_t s) {
+  constexpr int kOutputs = USE == kDw ? 2 : 1;
+  auto tiles = [&](int64_t tm, int64_t tn) { return ceil_div(a.m, tm) * ceil_div(a.n, tn) * kOutputs; };
+  constexpr int kHalf = USE == kForward ? 2 : 1;
+  // a tile has more than half its rows and columns to do; along the columns it must fit its operand
+  auto fits = [&](int64_t side) {
+    return a.m > (USE == kDw ? side - 1 : side / 2) && a.n > (USE != kForward ? side - 1 : side / kHalf / 2);
+  };
+  a.splits = 1;
+  a.partial = nullptr;
+  if (fits(256) && tiles(256, 256 / kHalf) >= kEnoughTiles) {
+    if constexpr (USE == kForward) return fetch_launch<USE, 2, 4, 4, 2, DT, ODT>(a, s);
+    else return fetch_launch<USE, 4, 2, 2, 4, DT, ODT>(a, s);
+  }
+  const bool middle = fits(128) && tiles(128, 128 / kHalf) >= kEnoughTiles;
+  if constexpr (USE != kForward) {
+    // few tiles over a long contraction: shared among blocks, as far as the scratch holds their sums
+    const int64_t have = middle ? tiles(128, 128) : tiles(64, 128);
+    const int64_t chunks = ceil_div(a.k, kChunk) * (USE == kDx ? 2 : 1);
+    int64_t splits = 512 / have;
+    splits = splits < chunks / 4 ? splits : chunks / 4;
+    const int64_t room = static_cast<int64_t>(kScratchBytes / sizeof(float)) / (a.m * a.n * kOutputs);
+    splits = splits < room ? splits : room;
+    if (splits > 1) {
+      a.splits = static_cast<int32_t>(splits);
+      a.partial = scratch;
+    }
+  }
+  hipError_t e;
+  if (middle) e = fetch_launch<USE, 2, 2, 2, 2, DT, ODT>(a, s);
+  else e = fetch_launch<USE, 1, 2, 2, 2, DT, ODT>(a, s);
+  if (e != hipSuccess || a.splits <= 1) return e;
+  const int64_t blocks = ceil_div(a.m * a.n, 256);
+  hipLaunchKernelGGL((gated_join_kernel<ODT>), dim3(static_cast<uint32_t>(blocks < 4096 ? blocks : 4096), kOutputs), dim3(256),
+                     0, s, a, kOutputs);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t forward_launch(const GatedArgs& g, hipStream_t s) {
+  ProductArgs a = {};
+  a.a[0] = static_cast<const char*>(g.x.p);
+  a.a_ld = g.x.ld * 2;
+  for (int i = 0; i < 2; ++i) a.b[i] = static_cast<const char*>(g.w[i].p);
+  a.b_ld = g.w[0].ld * 2;
+  a.m = g.m;
+  a.n = g.f;
+  a.k = g.d;
+  for (int i = 0; i < 3; ++i) {
+    a.out[i] = g.out[i].p;
+    a.out_ld[i] = g.out[i].ld;
+  }
+  a.act = g.act;
+  return product_launch<kForward, DT, DT>(a, nullptr, s);
+}
+
+template <int DT>
+hipError_t grad_launch(const GatedGradArgs& g, hipStream_t s) {
+  if (g.m > 0 && g.f > 0) {
+    GateGradArgs e = {g.dh, {g.pre[0], g.pre[1]}, {g.dpre[0], g.dpre[1]}, g.m, g.f, g.act};
+    if (g.dh.ld == g.f && g.pre[0].ld == g.f && g.dpre[0].ld == g.f) {  // one row
+      e.cols *= e.rows;
+      e.rows = 1;
+    }
+    const int64_t row_slots = ceil_div(e.cols, Vec<DT>::kVals), slots = row_slots * e.rows, blocks = ceil_div(slots, 256);
+    const int grid = limit_grid(static_cast<int>(blocks < kMaxGrid ? blocks : kMaxGrid));
+    hipLaunchKernelGGL((gate_grad_kernel<DT>), dim3(grid), dim3(256), 0, s, e, row_slots, slots);
+    if (hipError_t x = hipGetLastError()) return x;
+  }
+  ProductArgs a = {};
+  if (g.dx.p && g.m > 0 && g.d > 0) {
+    for (int i = 0; i < 2; ++i) {
+      a.a[i] = static_cast<const char*>(g.dpre[i].p);
+      a.b[i] = static_cast<const char*>(g.w[i].p);
+    }
+    a.a_ld = g.dpre[0].ld * 2;
+    a.b_ld = g.w[0].ld * 2;
+    a.m = g.m;
+    a.n = g.d;
+    a.k = g.f;
+    a.out[0] = g.dx.p;
+    a.out_ld[0] = g.dx.ld;
+    if (hipError_t e = product_launch<kDx, DT, DT>(a, g.scratch, s)) return e;
+  }
+  if (g.dw[0].p && g.f > 0 && g.d > 0) {
+    a = {};
+    for (int i = 0; i < 2; ++i) {
+      a.a[i] = static_cast<const char*>(g.dpre[i].p);
+      a.out[i] = g.dw[i].p;
+      a.out_ld[i] = g.dw[i].ld;
+    }
+    a.b[0] = static_cast<const char*>(g.x.p);
+    a.a_ld = g.dpre[0].ld * 2;
+    a.b_ld = g.x.ld * 2;
+    a.m = g.f;
+    a.n = g.d;
+    a.k = g.m;
+    a.accumulate = g.accumulate;
+    if (g.dw_dt == ZERO_DT_F32) return product_launch<kDw, DT, ZERO_DT_F32>(a, g.scratch, s);
+    return product_launch<kDw, DT, DT>(a, g.scratch, s);
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_gated(const GatedArgs& a, int32_t dt, hipStream_t s) {
+  if (dt == ZERO_DT_F16) return forward_launch<ZERO_DT_F16>(a, s);
+  if (dt == ZERO_DT_BF16) return forward_launch<ZERO_DT_BF16>(a, s);
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_gated_grad(const GatedGradArgs& a, int32_t dt, hipStream_t s) {
+  if (dt == ZERO_DT_F16) return grad_launch<ZERO_DT_F16>(a, s);
+  if (dt == ZERO_DT_BF16) return grad_launch<ZERO_DT_BF16>(a, s);
+  return hipErrorInvalidValue;
+}
+
+}  // namespace zdp

@@ -2,6 +2,8 @@
 #include <hip/hip_runtime.h>
 #include <math.h>
 
+#include <initializer_list>
+
 #include "api_common.h"
 #include "layer_internal.h"
 
@@ -45,6 +47,27 @@ int check_vector(const char* what, const void* p, int32_t dt, bool wanted) {
   if (!aligned(p, static_cast<uintptr_t>(dt_bytes(dt))))
     return fail(ZERO_ERR_ALIGNMENT, "%s is not aligned to its elements", what);
   return ZERO_OK;
+}
+
+int check_gated(int32_t dt, int64_t m, int64_t d, int64_t f, int32_t act) {
+  if (m < 0 || d < 0 || f < 0) return fail(ZERO_ERR_INVALID_ARG, "m, d or f < 0");
+  if (dt != ZERO_DT_F16 && dt != ZERO_DT_BF16) return fail(ZERO_ERR_INVALID_ARG, "x: dtype %d is not f16/bf16", dt);
+  if (act < ZERO_ACT_SILU || act > ZERO_ACT_SIGMOID) return fail(ZERO_ERR_INVALID_ARG, "act = %d", act);
+  if (m > INT32_MAX || d > INT32_MAX || f > INT32_MAX)
+    return fail(ZERO_ERR_UNSUPPORTED, "more than 2^31 - 1 rows or columns");
+  return ZERO_OK;
+}
+
+int check_strides(std::initializer_list<int64_t> lds) {
+  for (int64_t ld : lds)
+    if (ld > kMaxRowStride)
+      return fail(ZERO_ERR_UNSUPPORTED, "rows more than %lld elements apart", (long long)kMaxRowStride);
+  return ZERO_OK;
+}
+
+int launched(hipError_t e, const char* what) {
+  if (e == hipErrorInvalidConfiguration) return fail(ZERO_ERR_UNSUPPORTED, "more output tiles than a launch holds");
+  return e == hipSuccess ? ZERO_OK : hip_fail(e, what);
 }
 
 }  // namespace
@@ -155,6 +178,88 @@ int zero_dropout(const void* x, int32_t dt, int64_t rows, int64_t cols, int64_t 
   D.counter = counter;
   hipError_t e = launch_dropout(D, dt, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? ZERO_OK : hip_fail(e, "dropout launch");
+}
+
+int zero_gated_product(const void* x, int32_t dt, int64_t m, int64_t d, int64_t x_ld, const void* w_gate,
+                       const void* w_up, int64_t f, int64_t w_ld, int32_t act, void* h, int64_t h_ld, void* gate,
+                       void* up, int64_t pre_ld, void* stream) {
+  if (int rc = check_gated(dt, m, d, f, act)) return rc;
+  if (int rc = check_rows("x", x, dt, m, d, x_ld)) return rc;
+  if (int rc = check_rows("w_gate", w_gate, dt, f, d, w_ld)) return rc;
+  if (int rc = check_rows("w_up", w_up, dt, f, d, w_ld)) return rc;
+  if (int rc = check_rows("h", h, dt, m, f, h_ld)) return rc;
+  if ((gate == nullptr) != (up == nullptr)) return fail(ZERO_ERR_INVALID_ARG, "gate and up must be given together");
+  if (gate) {
+    if (int rc = check_rows("gate", gate, dt, m, f, pre_ld)) return rc;
+    if (int rc = check_rows("up", up, dt, m, f, pre_ld)) return rc;
+  }
+  if (m == 0 || f == 0) return ZERO_OK;
+  if (int rc = check_strides({x_ld, w_ld})) return rc;
+  if (int rc = check_device()) return rc;
+  GatedArgs G;
+  G.x = {x, x_ld};
+  G.w[0] = {w_gate, w_ld};
+  G.w[1] = {w_up, w_ld};
+  G.m = m;
+  G.d = d;
+  G.f = f;
+  G.act = act;
+  G.out[0] = {h, h_ld};
+  G.out[1] = {gate, pre_ld};
+  G.out[2] = {up, pre_ld};
+  return launched(launch_gated(G, dt, static_cast<hipStream_t>(stream)), "gated product launch");
+}
+
+int zero_gated_product_backward(const void* dh, int64_t dh_ld, const void* x, int32_t dt, int64_t m, int64_t d,
+                                int64_t x_ld, const void* w_gate, const void* w_up, int64_t f, int64_t w_ld, int32_t act,
+                                const void* gate, const void* up, int64_t pre_ld, void* dgate, void* dup,
+                                int64_t dpre_ld, void* dx, int64_t dx_ld, void* dw_gate, void* dw_up, int64_t dw_ld,
+                                int32_t dw_dt, int32_t accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+  if (int rc = check_gated(dt, m, d, f, act)) return rc;
+  if (int rc = check_rows("dh", dh, dt, m, f, dh_ld)) return rc;
+  if (int rc = check_rows("gate", gate, dt, m, f, pre_ld)) return rc;
+  if (int rc = check_rows("up", up, dt, m, f, pre_ld)) return rc;
+  if (int rc = check_rows("dgate", dgate, dt, m, f, dpre_ld)) return rc;
+  if (int rc = check_rows("dup", dup, dt, m, f, dpre_ld)) return rc;
+  if (dx) {
+    if (int rc = check_rows("dx", dx, dt, m, d, dx_ld)) return rc;
+    if (int rc = check_rows("w_gate", w_gate, dt, f, d, w_ld)) return rc;
+    if (int rc = check_rows("w_up", w_up, dt, f, d, w_ld)) return rc;
+    if (int rc = check_strides({w_ld})) return rc;
+  }
+  if ((dw_gate == nullptr) != (dw_up == nullptr))
+    return fail(ZERO_ERR_INVALID_ARG, "dw_gate and dw_up must be given together");
+  if (dw_gate) {
+    if (dw_dt != dt && dw_dt != ZERO_DT_F32)
+      return fail(ZERO_ERR_INVALID_ARG, "dw_gate: dtype %d is neither x's %d nor f32", dw_dt, dt);
+    if (int rc = check_rows("x", x, dt, m, d, x_ld)) return rc;
+    if (int rc = check_rows("dw_gate", dw_gate, dw_dt, f, d, dw_ld)) return rc;
+    if (int rc = check_rows("dw_up", dw_up, dw_dt, f, d, dw_ld)) return rc;
+    if (int rc = check_strides({x_ld})) return rc;
+  }
+  if (int rc = check_strides({dpre_ld})) return rc;
+  if (int rc = check_workspace(workspace, workspace_bytes)) return rc;
+  if (int rc = check_device()) return rc;
+  GatedGradArgs G;
+  G.dh = {dh, dh_ld};
+  G.x = {x, x_ld};
+  G.w[0] = {w_gate, w_ld};
+  G.w[1] = {w_up, w_ld};
+  G.pre[0] = {gate, pre_ld};
+  G.pre[1] = {up, pre_ld};
+  G.m = m;
+  G.d = d;
+  G.f = f;
+  G.act = act;
+  G.dpre[0] = {dgate, dpre_ld};
+  G.dpre[1] = {dup, dpre_ld};
+  G.dx = {dx, dx_ld};
+  G.dw[0] = {dw_gate, dw_ld};
+  G.dw[1] = {dw_up, dw_ld};
+  G.dw_dt = dw_dt;
+  G.accumulate = accumulate != 0;
+  G.scratch = reinterpret_cast<float*>(scratch_of(workspace));
+  return launched(launch_gated_grad(G, dt, static_cast<hipStream_t>(stream)), "gated product gradient launch");
 }
 
 }  // extern "C"
