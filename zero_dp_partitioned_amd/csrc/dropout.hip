@@ -9,7 +9,9 @@
 namespace zdp {
 namespace {
 
-constexpr int kSlots = 4;  // 16-byte slots a lane handles, all loads first
+constexpr int kSlots = 2;  // 16-byte slots a lane handles, all loads first
+// Tensors from 64 MiB on are read with the non-temporal hint.
+constexpr int64_t kOnceSlots = (64 << 20) / 16;
 
 __device__ __forceinline__ u4 philox(uint64_t block, uint64_t offset, uint64_t seed) {
   uint32_t c0 = static_cast<uint32_t>(block), c1 = static_cast<uint32_t>(block >> 32);
@@ -31,7 +33,7 @@ __device__ __forceinline__ u4 philox(uint64_t block, uint64_t offset, uint64_t s
 // A slot is 16 bytes of a row, and starts on a block of the generator: with an
 // index off a multiple of four it is the memory accesses that are off 16 bytes
 // (which costs them a line in nine), not the generator that runs twice.
-template <int DT, bool RESIDUAL>
+template <int DT, bool RESIDUAL, bool ONCE>
 __global__ void __launch_bounds__(256) dropout_kernel(const DropoutArgs D, int64_t row_slots, int64_t slots) {
   constexpr int kVals = Vec<DT>::kVals, kElem = Vec<DT>::kElem;
   uint64_t offset = D.offset;
@@ -55,9 +57,9 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropoutArgs D, int64
       x[q] = r[q] = (u4){0, 0, 0, 0};
       if (s >= slots) col[q] = D.cols;
       if (col[q] < 0 || col[q] >= D.cols) continue;
-      x[q] = load_part<DT>(static_cast<const char*>(D.x.p) + (row[q] * D.x.ld + col[q]) * kElem, D.cols - col[q]);
+      x[q] = load_part<DT, ONCE>(static_cast<const char*>(D.x.p) + (row[q] * D.x.ld + col[q]) * kElem, D.cols - col[q]);
       if constexpr (RESIDUAL)
-        r[q] = load_part<DT>(static_cast<const char*>(D.residual.p) + (row[q] * D.residual.ld + col[q]) * kElem,
+        r[q] = load_part<DT, ONCE>(static_cast<const char*>(D.residual.p) + (row[q] * D.residual.ld + col[q]) * kElem,
                              D.cols - col[q]);
     }
 #pragma unroll
@@ -111,8 +113,9 @@ hipError_t dropout_launch(DropoutArgs a, hipStream_t s) {
   const int64_t row_slots = ceil_div(a.cols + lead, Vec<DT>::kVals), slots = row_slots * a.rows;
   const int64_t blocks = ceil_div(slots, 256 * kSlots);
   const int grid = limit_grid(static_cast<int>(blocks < kMaxGrid ? blocks : kMaxGrid));
-  if (a.residual.p) hipLaunchKernelGGL((dropout_kernel<DT, true>), dim3(grid), dim3(256), 0, s, a, row_slots, slots);
-  else hipLaunchKernelGGL((dropout_kernel<DT, false>), dim3(grid), dim3(256), 0, s, a, row_slots, slots);
+  const auto kernel = slots >= kOnceSlots ? (a.residual.p ? dropout_kernel<DT, true, true> : dropout_kernel<DT, false, true>)
+                                          : (a.residual.p ? dropout_kernel<DT, true, false> : dropout_kernel<DT, false, false>);
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, s, a, row_slots, slots);
   return hipGetLastError();
 }
 

@@ -2,7 +2,7 @@
 //   g = x wg^T,  u = x wu^T,  h = act(g) * u,
 //   dg = dh act'(g) u,  du = dh act(g),
 //   dx = dg wg + du wu,  dwg = dg^T x,  dwu = du^T x,
-// in fp16 or bf16 on v_mfma_f32_32x32x16 (fp32 sums). The products are three
+// in fp16 or bf16 on v_mfma_f32_16x16x32 (fp32 sums). The products are three
 // uses of one tile kernel, which differ in how their operands lie in memory:
 //   forward  A = x, B = wg and wu side by side: contraction along the rows of both;
 //   dx       A = dg then du, along its rows; B = wg then wu, along its columns;
@@ -18,7 +18,6 @@
 namespace zdp {
 namespace {
 
-typedef float v16f __attribute__((ext_vector_type(16)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 typedef short s8 __attribute__((ext_vector_type(8)));
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
@@ -31,9 +30,9 @@ enum Use { kForward, kDx, kDw };
 // (aligned to elements), kMasked value by value (a dimension smaller than the tile).
 enum Fetch { kDirect, kStaged, kMasked };
 
-constexpr int kFrag = 32;      // rows of an operand per instruction
+constexpr int kFrag = 16;      // rows of an operand per instruction
 constexpr int kChunk = 64;     // contraction per stage: 128 bytes of a row
-constexpr int kSteps = 4;      // of 16, per chunk
+constexpr int kSteps = 2;      // of 32, per chunk
 constexpr int kPiece = 1024;   // bytes that a wave moves at a time
 constexpr int kPieceRows = 8;  // rows, or as much of the contraction as a piece's columns leave, of a piece
 
@@ -106,11 +105,11 @@ __device__ __forceinline__ void activation_grad(float g, int32_t act, float* a, 
 // ------------------------------------------------------------------------
 
 template <int DT>
-__device__ __forceinline__ v16f mfma(s8 b, s8 a, v16f c) {
+__device__ __forceinline__ f4 mfma(s8 b, s8 a, f4 c) {
   if constexpr (DT == ZERO_DT_BF16)
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, b), __builtin_bit_cast(b8, a), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, b), __builtin_bit_cast(b8, a), c, 0, 0, 0);
   else
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, b), __builtin_bit_cast(h8, a), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, b), __builtin_bit_cast(h8, a), c, 0, 0, 0);
 }
 
 __device__ __forceinline__ s8 read16(uint32_t lds) {
@@ -149,8 +148,8 @@ __device__ __forceinline__ void fetch_to_lds_if(uint32_t i, uint32_t n, const ch
 // runs, and inside a run in columns of kGroup tile rows, so that the tiles that
 // an XCD's 32 CUs work on at a time share their operands in its L2.
 constexpr int kXcds = 8;
-constexpr int kGroup = 8;
 
+template <uint32_t kGroup>
 __device__ __forceinline__ void tile_of(uint32_t b, uint32_t tm, uint32_t tn, uint32_t* m, uint32_t* n) {
   const uint32_t total = tm * tn, q = total / kXcds, rem = total % kXcds;
   const uint32_t x = b % kXcds;
@@ -188,21 +187,21 @@ struct Operand {
   static __device__ __forceinline__ int line(int p, int lane) { return p * kPieceLines + lane / kSlots; }
   static __device__ __forceinline__ int slot(int p, int lane) { return (lane % kSlots) ^ mix(line(p, lane)); }
 
-  // Where a lane reads fragment rows (columns) first .. first + 31 of step 0;
-  // `first` is a multiple of 32.
+  // Where a lane reads fragment rows (columns) first .. first + 15 of step 0;
+  // `first` is a multiple of 16.
   static __device__ __forceinline__ uint32_t fragment(int first, int lane) {
     if constexpr (!COLS) {
-      return (first + (lane & 31)) * kLine + ((lane >> 5) ^ mix(lane & 31)) * 16;
+      return (first + (lane & 15)) * kLine + ((lane >> 4) ^ mix(lane & 15)) * 16;
     } else {
-      const int k = 8 * (lane >> 5) + (lane >> 2 & 3);
-      return k * kLine + ((first / 8 + 2 * (lane >> 4 & 1) + (lane >> 1 & 1)) ^ mix(k)) * 16 + (lane & 1) * 8;
+      const int k = 8 * (lane >> 4) + (lane >> 2 & 3);
+      return k * kLine + ((first / 8 + (lane >> 1 & 1)) ^ mix(k)) * 16 + (lane & 1) * 8;
     }
   }
   static __device__ __forceinline__ s8 read(uint32_t at, int step) {
     if constexpr (!COLS) {
-      return read16(at ^ (step * 32));  // slots 2 * step + ...: the mix is an exclusive or
+      return read16(at ^ (step * 64));  // slots 4 * step + ...: the mix is an exclusive or
     } else {
-      const s4 lo = read_tr(at + step * 16 * kLine), hi = read_tr(at + (step * 16 + 4) * kLine);
+      const s4 lo = read_tr(at + step * 32 * kLine), hi = read_tr(at + (step * 32 + 4) * kLine);
       return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
   }
@@ -216,7 +215,7 @@ struct Operand {
 // same of wu, so that a lane holds g and u of the same outputs.
 // ------------------------------------------------------------------------
 
-template <Use USE, int FM, int FN, int WM, int WN>
+template <Use USE, int FM, int FN, int WM, int WN, int kBuffers = 2>
 struct Tile {
   static constexpr int kM = kFrag * FM * WM, kN = kFrag * FN * WN;
   static constexpr int kOutN = USE == kForward ? kN / 2 : kN;  // columns of an output
@@ -228,8 +227,8 @@ struct Tile {
   static constexpr int kStage = A::kBytes + B::kBytes;
   static constexpr int kRunN = kOutN / WN;  // columns of a wave's output
   static constexpr int kOutRow = kRunN + 4;  // floats, padded
-  static constexpr int kOut = kWaves * kFrag * kOutRow * 4;
-  static constexpr int kLds = 2 * kStage > kOut ? 2 * kStage : kOut;
+  static constexpr int kOut = kWaves * 2 * kFrag * kOutRow * 4;
+  static constexpr int kLds = kBuffers * kStage > kOut ? kBuffers * kStage : kOut;
   static_assert(kLds <= 160 * 1024, "LDS of a CU");
   static_assert(kPiecesA % kWaves == 0 && kPiecesB % kWaves == 0, "a load's pieces belong to one operand");
 };
@@ -238,9 +237,9 @@ __device__ __forceinline__ uint32_t tiles_of(int64_t n, uint32_t size) { return 
 
 // Registers: two waves a SIMD (256 each) for the largest tile, of which one
 // block fills a CU; more blocks of the smaller ones.
-template <Use USE, Fetch FETCH, int FM, int FN, int WM, int WN, int DT, int ODT>
+template <Use USE, Fetch FETCH, int FM, int FN, int WM, int WN, int NB, int DT, int ODT>
 __global__ void __launch_bounds__(64 * WM * WN, 2) gated_tile_kernel(const ProductArgs P) {
-  using T = Tile<USE, FM, FN, WM, WN>;
+  using T = Tile<USE, FM, FN, WM, WN, NB>;
   using A = typename T::A;
   using B = typename T::B;
   extern __shared__ __align__(1024) uint8_t lds[];
@@ -250,7 +249,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gated_tile_kernel(const Produ
   const uint32_t rows = USE == kDw ? 2 * tiles_m : tiles_m;  // dwu's tiles behind dwg's
   const uint32_t split = P.splits > 1 ? blockIdx.x / (rows * tiles_n) : 0;
   uint32_t tm, tn;
-  tile_of(P.splits > 1 ? blockIdx.x % (rows * tiles_n) : blockIdx.x, rows, tiles_n, &tm, &tn);
+  // (4 or 8 tile rows a group, us at 8192 x 4096 x 14336: forward 1457 or 1414, dx 1416 or 1365, dw 1379 or 1439)
+  tile_of<USE == kDw ? 4 : 8>(P.splits > 1 ? blockIdx.x % (rows * tiles_n) : blockIdx.x, rows, tiles_n, &tm, &tn);
   const int z = USE == kDw && tm >= tiles_m;  // which output
   if (z) tm -= tiles_m;
   // The tile's first row and column, and the first of the operands': along the
@@ -336,17 +336,28 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gated_tile_kernel(const Produ
   for (int f = 0; f < FM; ++f) aat[f] = lds0 + A::fragment((wm * FM + f) * kFrag, lane);
 #pragma unroll
   for (int f = 0; f < FN; ++f) bat[f] = lds0 + A::kBytes + B::fragment((wn * FN + f) * kFrag, lane);
-  s8 a[2][FM], b[2][FN];
-  // Fragment f of step s of the stage in `buffer`: B's first two, A's first, then
-  // the rest, in the order in which the products need them.
-  auto read = [&](uint32_t buffer, int s, int f) {
+  // Of the operand with more fragments (`ring`) a few are held ahead of their
+  // products, of the other one (`kept`) this step's and the next step's.
+  constexpr bool kRingA = FM > FN;
+  constexpr int kRing = kRingA ? FM : FN, kKept = kRingA ? FN : FM;
+  constexpr int kHeld = 4;                     // fragments of the ring in registers
+  constexpr int kAhead = kRing >= 8 ? 3 : 2;   // groups of products from a read to its use
+  static_assert(kRing % kHeld == 0 && kAhead < kHeld, "");
+  s8 ring[kHeld], kept[2][kKept];
+  auto read_ring = [&](uint32_t buffer, int s, int f) {
     const uint32_t at = buffer * T::kStage;
-    if (f < 2) b[s & 1][f] = B::read(bat[f] + at, s);
-    else if (f == 2) a[s & 1][0] = A::read(aat[0] + at, s);
-    else if (f <= FN) b[s & 1][f - 1] = B::read(bat[f - 1] + at, s);
-    else a[s & 1][f - FN] = A::read(aat[f - FN] + at, s);
+    ring[f % kHeld] = kRingA ? A::read(aat[f % FM] + at, s) : B::read(bat[f % FN] + at, s);
   };
-  v16f acc[FM][FN] = {};
+  auto read_kept = [&](uint32_t buffer, int s, int f) {
+    const uint32_t at = buffer * T::kStage;
+    kept[s & 1][f] = kRingA ? B::read(bat[f % FN] + at, s) : A::read(aat[f % FM] + at, s);
+  };
+  f4 acc[FM][FN] = {};
+  auto product = [&](int s, int r, int k) {
+    const int x = kRingA ? r : k, y = kRingA ? k : r;
+    const s8 av = kRingA ? ring[r % kHeld] : kept[s & 1][k], bv = kRingA ? kept[s & 1][k] : ring[r % kHeld];
+    acc[x][y] = mfma<DT>(bv, av, acc[x][y]);
+  };
 
   // What is left behind the whole chunks, one run after the other.
   if (FETCH != kMasked && rest && split == 0) {
@@ -362,11 +373,13 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gated_tile_kernel(const Produ
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
 #pragma unroll
-        for (int f = 0; f < FM + FN; ++f) read(1, s, f);
+        for (int k = 0; k < kKept; ++k) read_kept(1, s, k);
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
+        for (int r = 0; r < kRing; ++r) {
+          read_ring(1, s, r);
 #pragma unroll
-          for (int j = 0; j < FN; ++j) acc[i][j] = mfma<DT>(b[s & 1][j], a[s & 1][i], acc[i][j]);
+          for (int k = 0; k < kKept; ++k) product(s, r, k);
+        }
       }
     }
     __syncthreads();
@@ -376,114 +389,126 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gated_tile_kernel(const Produ
     u4 pend[FETCH == kDirect ? 1 : T::kLoads];
     // Load j of stage i: into LDS if there is that stage, or (the last stage
     // again past the end) into registers.
-    auto fetch = [&](uint32_t i, int j) {
+    constexpr uint32_t kBuffers = FETCH == kDirect ? NB : 2;
+    uint32_t buffer = 0;  // of the stage that is worked on
+    auto buffer_of = [&](uint32_t ahead) {  // of the stage `ahead` of it
+      const uint32_t b = buffer + ahead;
+      return b < kBuffers ? b : b - kBuffers;
+    };
+    auto fetch = [&](uint32_t i, int j, uint32_t to) {
       if constexpr (FETCH == kDirect) {
         const uint32_t c = c0 + i;
         fetch_to_lds_if(i, stages, from(c, j), off[j],
-                        lds0 + (i & 1) * T::kStage + (j < T::kLoadsA ? 0 : A::kBytes) + piece(j) * kPiece);
+                        lds0 + to * T::kStage + (j < T::kLoadsA ? 0 : A::kBytes) + piece(j) * kPiece);
       } else {
         const uint32_t c = c0 + (i < stages ? i : stages - 1);
         if constexpr (FETCH == kStaged) pend[j] = load_any(from(c, j) + off[j]);
         else pend[j] = masked(kParts == 2 && c >= whole, kParts == 2 && c >= whole ? c - whole : c, j);
       }
     };
-    // Stage i, fetched, to every wave. All of them have read out its buffer's stage before.
-    auto publish = [&](uint32_t i) {
+    // Stage i, fetched into buffer `to`, to every wave. All of them have read out
+    // the stage that was there before. Up to kBuffers - 2 younger stages stay in flight.
+    auto publish = [&](uint32_t i, uint32_t to) {
       if constexpr (FETCH == kDirect) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        constexpr int kYounger = (kBuffers - 2) * T::kLoads;
+        if constexpr (kYounger > 0)
+          asm volatile(
+              "s_waitcnt vmcnt(%2)\n\ts_cmp_lt_u32 %0, %1\n\ts_cbranch_scc1 .Lzdp_some%=\n\ts_waitcnt vmcnt(0)\n.Lzdp_some%=:" ::"s"(
+                  i + kBuffers - 2),
+              "s"(stages), "i"(kYounger)
+              : "memory", "scc");
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       } else {
 #pragma unroll
-        for (int j = 0; j < T::kLoads; ++j) put(i & 1, j, pend[j]);
+        for (int j = 0; j < T::kLoads; ++j) put(to, j, pend[j]);
       }
       __syncthreads();
     };
-    constexpr int kPer = FM * FN >= 4 ? 2 : 1;          // products of a group
-    constexpr int kGroups = FM * FN / kPer;             // per step
-    constexpr int kReads = (FM + FN + kGroups - 1) / kGroups;            // per group
-    constexpr int kLateReads = (FM + FN + kGroups - 2) / (kGroups - 1);  // per group of the last step but its first
-    constexpr int kFetches = (T::kLoads + 2 * kGroups) / (2 * kGroups + 1);
-    // One step: per group its products and a few reads of the next step's
-    // fragments, the order fixed so that reads and products leave in turn. The
-    // last step publishes the next stage behind its first group (every wave has
-    // read this stage out by then) and starts fetching the one after it into
-    // this stage's place; the next stage's first steps fetch the rest. Stages
-    // that pass through registers are fetched in their predecessor's first steps.
+    // A step is a group of products for each fragment of the ring, and with each
+    // group the ring's fragment that is kAhead groups away is read, and some of
+    // the next step's kept ones; the order is fixed. Once the last step's own
+    // fragments have been asked for (group kTurn), the next stage is published,
+    // and what follows is read from there; the fetches of the stage after it
+    // start into this stage's place, one a group, and run on into the next
+    // stage's first step. Stages that pass through registers are fetched in their
+    // predecessor's first step.
+    constexpr int kTurn = kRing - kAhead;
     auto step = [&](auto sc, uint32_t i) {
       constexpr int S = decltype(sc)::value;
+      constexpr bool kLast = S == kSteps - 1;
 #pragma unroll
-      for (int t = 0; t < kGroups; ++t) {
-        if constexpr (S == kSteps - 1) {
-          if (t == 1) publish(i + 1);
-        }
+      for (int t = 0; t < kRing; ++t) {
+        if (kLast && t == kTurn) publish(i + 1, buffer_of(1));
         if constexpr (FETCH == kDirect) {
-          const int slot = S == kSteps - 1 ? t - 1 : kGroups - 1 + S * kGroups + t;
-#pragma unroll
-          for (int q = 0; q < kFetches; ++q)
-            if (slot >= 0 && slot * kFetches + q < T::kLoads) fetch(i + (S == kSteps - 1 ? 2 : 1), slot * kFetches + q);
-        } else if constexpr (S < 2) {
-          constexpr int kEach = (T::kLoads + 2 * kGroups - 1) / (2 * kGroups);
+          constexpr int kEach = (T::kLoads + kRing - 1) / kRing;
+          const int slot = kLast ? t - kTurn : kAhead + S * kRing + t;
 #pragma unroll
           for (int q = 0; q < kEach; ++q)
-            if ((S * kGroups + t) * kEach + q < T::kLoads) fetch(i + 1, (S * kGroups + t) * kEach + q);
+            if (slot >= 0 && slot * kEach + q < T::kLoads) fetch(i + kBuffers - (kLast ? 0 : 1), slot * kEach + q, kLast ? buffer : buffer_of(kBuffers - 1));
+        } else if constexpr (S == 0) {
+          constexpr int kEach = (T::kLoads + kRing - 1) / kRing;
+#pragma unroll
+          for (int q = 0; q < kEach; ++q)
+            if (t * kEach + q < T::kLoads) fetch(i + 1, t * kEach + q, 0);
         }
 #pragma unroll
-        for (int q = 0; q < kPer; ++q) {
-          const int x = (t * kPer + q) / FN, y = (t * kPer + q) % FN;
-          acc[x][y] = mfma<DT>(b[S & 1][y], a[S & 1][x], acc[x][y]);
-        }
-        if constexpr (S < kSteps - 1) {
+        for (int k = 0; k < kKept; ++k) product(S, t, k);
+        const bool next = kLast && t >= kTurn;  // the next stage's
+        read_ring(next ? buffer_of(1) : buffer, t < kTurn ? S : (S + 1) % kSteps, (t + kAhead) % kRing);
+        constexpr int kFirst = kLast ? kTurn : 0, kSpan = kLast ? kAhead - 1 : kRing - 1;  // groups with reads of kept ones
 #pragma unroll
-          for (int q = 0; q < kReads; ++q)
-            if (t * kReads + q < FM + FN) read(i & 1, S + 1, t * kReads + q);
-        } else if (t > 0) {
-#pragma unroll
-          for (int q = 0; q < kLateReads; ++q)
-            if ((t - 1) * kLateReads + q < FM + FN) read((i + 1) & 1, 0, (t - 1) * kLateReads + q);
-        }
+        for (int k = 0; k < kKept; ++k)
+          if (k * kSpan / kKept == t - kFirst) read_kept(next ? buffer_of(1) : buffer, (S + 1) % kSteps, k);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
 #pragma unroll
-    for (int j = 0; j < T::kLoads; ++j) fetch(0, j);
-    publish(0);
+    for (uint32_t q = 0; q < kBuffers - 1; ++q)
 #pragma unroll
-    for (int f = 0; f < FM + FN; ++f) read(0, 0, f);
+      for (int j = 0; j < T::kLoads; ++j) fetch(q, j, q);
+    publish(0, 0);
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) read_kept(0, 0, k);
+#pragma unroll
+    for (int r = 0; r < kAhead; ++r) read_ring(0, 0, r);
     if constexpr (FETCH == kDirect) {
-      constexpr int kEarly = (kGroups - 1) * kFetches < T::kLoads ? (kGroups - 1) * kFetches : T::kLoads;
+      constexpr int kEach = (T::kLoads + kRing - 1) / kRing;
+      constexpr int kEarly = kAhead * kEach < T::kLoads ? kAhead * kEach : T::kLoads;
 #pragma unroll
-      for (int j = 0; j < kEarly; ++j) fetch(1, j);
+      for (int j = 0; j < kEarly; ++j) fetch(kBuffers - 1, j, kBuffers - 1);
     }
     uint32_t i = 0;
     do {
       step(std::integral_constant<int, 0>{}, i);
       step(std::integral_constant<int, 1>{}, i);
-      step(std::integral_constant<int, 2>{}, i);
-      step(std::integral_constant<int, 3>{}, i);
+      buffer = buffer_of(1);
     } while (++i < stages);
     __syncthreads();
   }
 
   // 32 rows of the wave's part of the tile at a time, through LDS, so that a row
-  // leaves in runs of 16 bytes a lane. A lane holds columns 8 q + 4 (lane / 32) +
-  // 0..3 of row lane % 32 of a fragment.
-  float* const mine = reinterpret_cast<float*>(lds) + w * kFrag * T::kOutRow;
-  const int r = lane & 31, half = lane >> 5;
+  // leaves in runs of 16 bytes a lane. A lane holds columns 4 (lane / 16) + 0..3
+  // of row lane % 16 of a fragment.
+  constexpr int kBatch = 2;  // fragments
+  float* const mine = reinterpret_cast<float*>(lds) + w * kBatch * kFrag * T::kOutRow;
   auto rows_out = [&](auto type, int i, void* out, int64_t ld, bool add, auto&& value) {
     constexpr int O = decltype(type)::value, kVals = Vec<O>::kVals, kElem = Vec<O>::kElem;
-    constexpr int kFrags = T::kRunN / kFrag;
 #pragma unroll
-    for (int j = 0; j < kFrags; ++j)
+    for (int f = 0; f < kBatch; ++f)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int j = 0; j < T::kRunN / kFrag; ++j) {
         f4 x;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = value(j, 4 * q + e);
-        *reinterpret_cast<f4*>(mine + r * T::kOutRow + j * kFrag + 8 * q + 4 * half) = x;
+        for (int e = 0; e < 4; ++e) x[e] = value(i + f, j, e);
+        *reinterpret_cast<f4*>(mine + (f * kFrag + (lane & 15)) * T::kOutRow + j * kFrag + 4 * (lane >> 4)) = x;
       }
     __builtin_amdgcn_wave_barrier();
     constexpr int kRuns = T::kRunN / kVals;  // of a row
+    // Runs of whole lines go past the caches (8192 x 4096 x 4096 with h, g and u
+    // written: 435 -> 405 us; the products' operands keep their place there).
+    const bool whole_lines = ((reinterpret_cast<uintptr_t>(out) | static_cast<uintptr_t>(ld * kElem) | static_cast<uintptr_t>(bn0 * kElem)) & 15) == 0;
 #pragma unroll
-    for (int t = 0; t < kFrag * kRuns / 64; ++t) {
+    for (int t = 0; t < kBatch * kFrag * kRuns / 64; ++t) {
       const int row = (t * 64 + lane) / kRuns, col = (t * 64 + lane) % kRuns * kVals;
       float v[kVals];
 #pragma unroll
@@ -505,7 +530,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gated_tile_kernel(const Produ
           for (int e = 0; e < kVals; ++e) v[e] += old[e];
         }
         const u4 x = narrow<O>(v);
-        __builtin_memcpy(to, &x, 16);
+        if (whole_lines) __builtin_nontemporal_store(x, reinterpret_cast<u4*>(to));
+        else __builtin_memcpy(to, &x, 16);
       } else {
         if (add) {
 #pragma unroll
@@ -519,20 +545,136 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gated_tile_kernel(const Produ
   };
   using Type = std::integral_constant<int, ODT>;
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
+  for (int i = 0; i < FM; i += kBatch) {
     if constexpr (USE == kForward) {
       constexpr int H = FN / 2;
       rows_out(Type{}, i, P.out[0], P.out_ld[0], false,
-               [&](int j, int e) { return activation(acc[i][j][e], P.act) * acc[i][j + H][e]; });
+               [&](int i, int j, int e) { return activation(acc[i][j][e], P.act) * acc[i][j + H][e]; });
       if (P.out[1]) {
-        rows_out(Type{}, i, P.out[1], P.out_ld[1], false, [&](int j, int e) { return acc[i][j][e]; });
-        rows_out(Type{}, i, P.out[2], P.out_ld[2], false, [&](int j, int e) { return acc[i][j + H][e]; });
+        rows_out(Type{}, i, P.out[1], P.out_ld[1], false, [&](int i, int j, int e) { return acc[i][j][e]; });
+        rows_out(Type{}, i, P.out[2], P.out_ld[2], false, [&](int i, int j, int e) { return acc[i][j + H][e]; });
       }
     } else if (P.splits > 1) {
       float* const to = P.partial + (static_cast<int64_t>(split) * (USE == kDw ? 2 : 1) + z) * P.m * P.n;
-      rows_out(std::integral_constant<int, ZERO_DT_F32>{}, i, to, P.n, false, [&](int j, int e) { return acc[i][j][e]; });
+      rows_out(std::integral_constant<int, ZERO_DT_F32>{}, i, to, P.n, false, [&](int i, int j, int e) { return acc[i][j][e]; });
     } else {
-      rows_out(Type{}, i, P.out[z], P.out_ld[z], P.accumulate, [&](int j, int e) { return acc[i][j][e]; });
+      rows_out(Type{}, i, P.out[z], P.out_ld[z], P.accumulate, [&](int i, int j, int e) { return acc[i][j][e]; });
+    }
+  }
+}
+
+// ------------------------------------------------------------------------
+// Forward for very few rows, kTokens of them at most, which is one pass over the
+// weights: a block takes 16 rows of wg and the same of wu. A wave takes runs of
+// 512 of the contraction, 8 a lane, and goes through the block's rows, so that a
+// load is one contiguous KiB of a row whatever its alignment, and x stays in
+// registers; the next rows' loads are in flight while a few are worked on. The
+// lanes' sums are added once, at the end. Measured with 14336 x 4096 weights in
+// bf16: one row 41 us (5.7 TB/s; 4.3 times as much code in the sums over lanes
+// took 57), four 44, of the tiles 47 at any number up to 16. Fragments loaded
+// straight to the matrix instruction, 64 bytes of each of 16 rows a load, took 44
+// and 50 us for one and 16 rows.
+// ------------------------------------------------------------------------
+
+// N values a lane added over the 64 lanes, by halves: in each step every lane
+// hands half of its values over and keeps the sums of the other half. Lane l ends
+// with N / 64 values from l * N / 64 on, or 64 / N lanes with value l * N / 64.
+template <int N, int LANES>
+__device__ __forceinline__ void lanes_sums(float* v, int lane) {
+  if constexpr (LANES > 0) {
+    constexpr int kHalf = N / 2;
+    if constexpr (kHalf > 0) {
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) {
+        const float keep = lane & LANES ? v[i + kHalf] : v[i], give = lane & LANES ? v[i] : v[i + kHalf];
+        v[i] = keep + __shfl_xor(give, LANES, 64);
+      }
+      lanes_sums<kHalf, LANES / 2>(v, lane);
+    } else {
+      v[0] += __shfl_xor(v[0], LANES, 64);
+      lanes_sums<1, LANES / 2>(v, lane);
+    }
+  }
+}
+
+constexpr int64_t kTokens = 4;
+constexpr int kTokenRun = 512;
+constexpr int kTokenWaves = 4;  // of a block: with eight, four rows took 60 us instead of 44
+
+template <int T, int DT>
+__global__ void __launch_bounds__(64 * kTokenWaves) gated_token_kernel(const ProductArgs P) {
+  constexpr int NW = kTokenWaves, kValues = 2 * kFrag * T;
+  constexpr int kTogether = 4;  // rows of wg and of wu that are loaded at once (2 or 8: 47 and 60 us)
+  __shared__ float sums[NW][kValues];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kFrag;
+  const int last = P.n - 1 - n0 < kFrag - 1 ? static_cast<int>(P.n - 1 - n0) : kFrag - 1;
+  const char* const wg = P.b[0] + n0 * P.b_ld;
+  const char* const wu = P.b[1] + n0 * P.b_ld;
+  float acc[kValues] = {};  // of product z, row r, token t at (z * 16 + r) * T + t
+  for (int64_t run = static_cast<int64_t>(w) * kTokenRun; run < P.k; run += NW * kTokenRun) {
+    // a lane past the end, or that would pass it, takes the last 8 values; what another lane has is zero in x
+    const int64_t k = run + lane * 8, at = k < P.k - 8 ? k : P.k - 8;
+    const uint32_t off = static_cast<uint32_t>((at - run) * 2);
+    float x[T][8];
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      widen<DT>(load_any(P.a[0] + (t < P.m ? t : P.m - 1) * P.a_ld + at * 2), x[t]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[t][e] = e >= k - at ? x[t][e] : 0.f;
+    }
+    u4 v[2][2][kTogether];
+    auto fetch = [&](int r0, u4 (&to)[2][kTogether]) {
+#pragma unroll
+      for (int r = 0; r < kTogether; ++r) {
+        const int64_t row = r0 + r < last ? r0 + r : last;
+        to[0][r] = load_any(wg + row * P.b_ld + run * 2 + static_cast<int32_t>(off));
+        to[1][r] = load_any(wu + row * P.b_ld + run * 2 + static_cast<int32_t>(off));
+      }
+    };
+    fetch(0, v[0]);
+#pragma unroll
+    for (int r0 = 0; r0 < kFrag; r0 += kTogether) {
+      const int now = r0 / kTogether & 1;
+      if (r0 + kTogether < kFrag) fetch(r0 + kTogether, v[now ^ 1]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int z = 0; z < 2; ++z)
+#pragma unroll
+        for (int r = 0; r < kTogether; ++r) {
+          float y[8];
+          widen<DT>(v[now][z][r], y);
+#pragma unroll
+          for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float& s = acc[(z * kFrag + r0 + r) * T + t];
+              s = __builtin_fmaf(y[e], x[t][e], s);
+            }
+        }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  lanes_sums<kValues, 32>(acc, lane);
+  constexpr int kEach = kValues >= 64 ? kValues / 64 : 1, kLanes = kValues >= 64 ? 1 : 64 / kValues;  // values a lane, lanes a value
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) sums[w][lane / kLanes * kEach + i] = acc[i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < kFrag * T; i += 64 * NW) {
+    const int r = i / T, t = i % T;
+    if (t >= P.m || r > last) continue;
+    float g = 0.f, u = 0.f;
+#pragma unroll
+    for (int q = 0; q < NW; ++q) {
+      g += sums[q][i];
+      u += sums[q][kFrag * T + i];
+    }
+    const int64_t n = n0 + r;
+    store_one(P.out[0], t * P.out_ld[0] + n, DT, activation(g, P.act) * u);
+    if (P.out[1]) {
+      store_one(P.out[1], t * P.out_ld[1] + n, DT, g);
+      store_one(P.out[2], t * P.out_ld[2] + n, DT, u);
     }
   }
 }
@@ -569,9 +711,9 @@ __global__ void __launch_bounds__(256) gate_grad_kernel(const GateGradArgs G, in
   for (int64_t s = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; s < slots; s += static_cast<int64_t>(gridDim.x) * 256) {
     const int64_t row = G.rows > 1 ? s / row_slots : 0, col = (s - row * row_slots) * kVals, left = G.cols - col;
     float dh[kVals], g[kVals], u[kVals];
-    widen<DT>(load_part<DT>(static_cast<const char*>(G.dh.p) + (row * G.dh.ld + col) * 2, left), dh);
-    widen<DT>(load_part<DT>(static_cast<const char*>(G.pre[0].p) + (row * G.pre[0].ld + col) * 2, left), g);
-    widen<DT>(load_part<DT>(static_cast<const char*>(G.pre[1].p) + (row * G.pre[1].ld + col) * 2, left), u);
+    widen<DT>(load_part<DT, true>(static_cast<const char*>(G.dh.p) + (row * G.dh.ld + col) * 2, left), dh);
+    widen<DT>(load_part<DT, true>(static_cast<const char*>(G.pre[0].p) + (row * G.pre[0].ld + col) * 2, left), g);
+    widen<DT>(load_part<DT, true>(static_cast<const char*>(G.pre[1].p) + (row * G.pre[1].ld + col) * 2, left), u);
 #pragma unroll
     for (int e = 0; e < kVals; ++e) {
       float a, da;
@@ -588,10 +730,10 @@ __global__ void __launch_bounds__(256) gate_grad_kernel(const GateGradArgs G, in
 // Launches
 // ------------------------------------------------------------------------
 
-template <Use USE, Fetch FETCH, int FM, int FN, int WM, int WN, int DT, int ODT>
+template <Use USE, Fetch FETCH, int FM, int FN, int WM, int WN, int NB, int DT, int ODT>
 hipError_t tile_launch(const ProductArgs& a, hipStream_t s) {
-  using T = Tile<USE, FM, FN, WM, WN>;
-  const auto kernel = gated_tile_kernel<USE, FETCH, FM, FN, WM, WN, DT, ODT>;
+  using T = Tile<USE, FM, FN, WM, WN, NB>;
+  const auto kernel = gated_tile_kernel<USE, FETCH, FM, FN, WM, WN, NB, DT, ODT>;
   const int64_t tiles = ceil_div(a.m, T::kM) * ceil_div(a.n, T::kOutN) * (USE == kDw ? 2 : 1);
   if (tiles > INT32_MAX / T::kThreads / (a.splits > 1 ? a.splits : 1)) return hipErrorInvalidConfiguration;
   // more than the default limit of 64 KiB of dynamic LDS, granted once per kernel and device
@@ -613,26 +755,38 @@ hipError_t tile_launch(const ProductArgs& a, hipStream_t s) {
 bool aligned16(const void* p, int64_t ld_bytes) { return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld_bytes)) & 15) == 0; }
 
 constexpr int64_t kEnoughTiles = 160;
+constexpr int64_t kCus = 256;
+constexpr int64_t kFewSmall = 448;
 
-// One tile shape with the fetch that the operands allow.
-template <Use USE, int FM, int FN, int WM, int WN, int DT, int ODT>
+// One tile shape with the fetch that the operands allow; fetches that write LDS
+// themselves keep NB - 1 stages in flight.
+template <Use USE, int FM, int FN, int WM, int WN, int NB, int DT, int ODT>
 hipError_t fetch_launch(const ProductArgs& a, hipStream_t s) {
   using T = Tile<USE, FM, FN, WM, WN>;
-  if constexpr (FM == 1 && USE != kForward) {
-    if ((USE == kDw && a.m < T::kM) || a.n < T::kN) return tile_launch<USE, kMasked, FM, FN, WM, WN, DT, ODT>(a, s);
+  if constexpr (T::kM == 64 && USE != kForward) {
+    if ((USE == kDw && a.m < T::kM) || a.n < T::kN) return tile_launch<USE, kMasked, FM, FN, WM, WN, 2, DT, ODT>(a, s);
   }
   // a moved tile starts at n - kN: on 16 bytes if n is
   bool direct = aligned16(a.a[0], a.a_ld) && aligned16(a.b[0], a.b_ld) && (!a.a[1] || aligned16(a.a[1], a.a_ld)) &&
                 (!a.b[1] || aligned16(a.b[1], a.b_ld));
   if (USE == kDw) direct = direct && a.m % 8 == 0;
   if (USE != kForward) direct = direct && a.n % 8 == 0;
-  if (direct) return tile_launch<USE, kDirect, FM, FN, WM, WN, DT, ODT>(a, s);
-  return tile_launch<USE, kStaged, FM, FN, WM, WN, DT, ODT>(a, s);
+  if (direct) return tile_launch<USE, kDirect, FM, FN, WM, WN, NB, DT, ODT>(a, s);
+  return tile_launch<USE, kStaged, FM, FN, WM, WN, 2, DT, ODT>(a, s);
 }
 
 template <Use USE, int DT, int ODT>
 hipError_t product_launch(ProductArgs a, float* scratch, hipStream_t s) {
   constexpr int kOutputs = USE == kDw ? 2 : 1;
+  if constexpr (USE == kForward) {
+    if (a.m <= kTokens && a.k >= 8) {
+      const dim3 blocks(static_cast<uint32_t>(ceil_div(a.n, kFrag))), threads(64 * kTokenWaves);
+      if (a.m == 1) hipLaunchKernelGGL((gated_token_kernel<1, DT>), blocks, threads, 0, s, a);
+      else if (a.m == 2) hipLaunchKernelGGL((gated_token_kernel<2, DT>), blocks, threads, 0, s, a);
+      else hipLaunchKernelGGL((gated_token_kernel<4, DT>), blocks, threads, 0, s, a);
+      return hipGetLastError();
+    }
+  }
   auto tiles = [&](int64_t tm, int64_t tn) { return ceil_div(a.m, tm) * ceil_div(a.n, tn) * kOutputs; };
   constexpr int kHalf = USE == kForward ? 2 : 1;
   // a tile has more than half its rows and columns to do; along the columns it must fit its operand
@@ -642,8 +796,8 @@ hipError_t product_launch(ProductArgs a, float* scratch, hipStream_t s) {
   a.splits = 1;
   a.partial = nullptr;
   if (fits(256) && tiles(256, 256 / kHalf) >= kEnoughTiles) {
-    if constexpr (USE == kForward) return fetch_launch<USE, 2, 4, 4, 2, DT, ODT>(a, s);
-    else return fetch_launch<USE, 4, 2, 2, 4, DT, ODT>(a, s);
+    if constexpr (USE == kForward) return fetch_launch<USE, 4, 8, 4, 2, 2, DT, ODT>(a, s);
+    else return fetch_launch<USE, 8, 4, 2, 4, 2, DT, ODT>(a, s);
   }
   const bool middle = fits(128) && tiles(128, 128 / kHalf) >= kEnoughTiles;
   if constexpr (USE != kForward) {
@@ -660,11 +814,22 @@ hipError_t product_launch(ProductArgs a, float* scratch, hipStream_t s) {
     }
   }
   hipError_t e;
-  if (middle) e = fetch_launch<USE, 2, 2, 2, 2, DT, ODT>(a, s);
-  else e = fetch_launch<USE, 1, 2, 2, 2, DT, ODT>(a, s);
+  // A middle tile with a CU to itself takes eight waves and keeps three stages in
+  // flight; where there are two a CU, four waves and one stage each are as good (dx
+  // of 2000 x 2048 x 8000, 256 tiles: 215 us with four waves, 203 with eight, 138
+  // with three stages in flight too; forward of 128 x 4096 x 14336, 224: 74, 70, 58).
+  // The small tile has two stages in flight where its blocks do not fill the CUs
+  // (forward of 17 x 4096 x 14336, 224 blocks: 61 -> 47.5 us; dx of 1001 x 1600 x
+  // 6400, 416: 74 -> 65) and one where they do (dx of 16 x 4096 x 14336, 512: 46.5
+  // against 50).
+  const int64_t blocks = (middle ? tiles(128, 128 / kHalf) : tiles(64, 128 / kHalf)) * a.splits;
+  if (middle && blocks <= kCus) e = fetch_launch<USE, 2, 4, 4, 2, 4, DT, ODT>(a, s);
+  else if (middle) e = fetch_launch<USE, 4, 4, 2, 2, 2, DT, ODT>(a, s);
+  else if (blocks <= kFewSmall) e = fetch_launch<USE, 2, 4, 2, 2, 3, DT, ODT>(a, s);
+  else e = fetch_launch<USE, 2, 4, 2, 2, 2, DT, ODT>(a, s);
   if (e != hipSuccess || a.splits <= 1) return e;
-  const int64_t blocks = ceil_div(a.m * a.n, 256);
-  hipLaunchKernelGGL((gated_join_kernel<ODT>), dim3(static_cast<uint32_t>(blocks < 4096 ? blocks : 4096), kOutputs), dim3(256),
+  const int64_t join = ceil_div(a.m * a.n, 256);
+  hipLaunchKernelGGL((gated_join_kernel<ODT>), dim3(static_cast<uint32_t>(join < 4096 ? join : 4096), kOutputs), dim3(256),
                      0, s, a, kOutputs);
   return hipGetLastError();
 }

@@ -82,10 +82,15 @@ __device__ __forceinline__ T load_any(const void* p) {
   return x;
 }
 
+// The same with the non-temporal hint: data that a pass touches once.
+typedef u4 u4_any __attribute__((aligned(2)));
+__device__ __forceinline__ u4 load_once(const void* p) { return __builtin_nontemporal_load(static_cast<const u4_any*>(p)); }
+__device__ __forceinline__ void store_once(void* p, u4 x) { __builtin_nontemporal_store(x, static_cast<u4_any*>(p)); }
+
 // The values at p, as far as `left` of them exist; the rest 0.
-template <int DT, typename Left>
+template <int DT, bool ONCE = false, typename Left>
 __device__ __forceinline__ u4 load_part(const char* p, Left left) {
-  if (left >= Vec<DT>::kVals) return load_any(p);
+  if (left >= Vec<DT>::kVals) return ONCE ? load_once(p) : load_any(p);
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int q = 0; q < Vec<DT>::kVals; ++q)
@@ -110,7 +115,7 @@ __device__ __forceinline__ void store_some(char* p, int first, int end, u4 x) {
 
 template <int DT, typename Left>
 __device__ __forceinline__ void store_part(char* p, Left left, u4 x) {
-  if (left >= Vec<DT>::kVals) __builtin_memcpy(p, &x, 16);
+  if (left >= Vec<DT>::kVals) store_once(p, x);
   else store_some<DT>(p, 0, static_cast<int>(left), x);
 }
 

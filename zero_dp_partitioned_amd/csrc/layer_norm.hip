@@ -75,9 +75,10 @@ struct Slot {
     skip = col - at;
   }
   __device__ __forceinline__ u4 load(const char* row) const { return load_any(row + at * Vec<DT>::kElem); }
+  __device__ __forceinline__ u4 load_once(const char* row) const { return zdp::load_once(row + at * Vec<DT>::kElem); }
   __device__ __forceinline__ void store(char* row, u4 x) const {
     char* const p = row + at * Vec<DT>::kElem;
-    if (skip == 0) __builtin_memcpy(p, &x, 16);
+    if (skip == 0) store_once(p, x);
     else store_some<DT>(p, skip, Vec<DT>::kVals, x);
   }
 };
@@ -197,13 +198,35 @@ __host__ __device__ inline int64_t sums_pitch(int64_t cols) { return (cols + 3) 
 // leaves one row of sums. The next row's loads are in flight while a row is
 // worked on. A block's groups take equally many turns, so that its barriers meet.
 template <int DT, int V, int W, int G, bool RES>
-__global__ void __launch_bounds__(64 * W * G, V <= 2 ? 4 : 2) norm_grad_kernel(const NormGradArgs N) {
+__global__ void __launch_bounds__(64 * W * G, 2) norm_grad_kernel(const NormGradArgs N) {
   constexpr int kVals = Vec<DT>::kVals, kElem = Vec<DT>::kElem;
   __shared__ float part[2][2][G][W];
-  __shared__ f4 sums[G > 1 ? 64 * W * V * kVals / 4 * 2 : 1];
+  __shared__ f4 sums[G > 1 ? (G - 1) * 64 * W * V * kVals / 4 * 2 : 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = wave / W, w = wave % W;
   const float inv = 1.0f / static_cast<float>(N.cols);
   auto slot = [&](int j) { return Slot<DT, W>(j, w, lane, N.cols); };
+  u4 x[V], dy[V], res[V];
+  float next_mean, next_rstd;
+  auto fetch = [&](int64_t row) {  // the last row again past it
+    row = row < N.rows ? row : N.rows - 1;
+    next_mean = N.mean[row];
+    next_rstd = N.rstd[row];
+    const char* const px = static_cast<const char*>(N.x.p) + row * N.x.ld * kElem;
+    const char* const pd = static_cast<const char*>(N.dy.p) + row * N.dy.ld * kElem;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      x[j] = slot(j).load_once(px);
+      dy[j] = slot(j).load_once(pd);
+    }
+    if (RES) {
+      const char* const pr = static_cast<const char*>(N.dresidual.p) + row * N.dresidual.ld * kElem;
+#pragma unroll
+      for (int j = 0; j < V; ++j) res[j] = slot(j).load_once(pr);
+    }
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * G + g;
+  fetch(row);
   float weight[V][kVals], dw[V][kVals] = {}, db[V][kVals] = {};
 #pragma unroll
   for (int j = 0; j < V; ++j) {
@@ -213,29 +236,10 @@ __global__ void __launch_bounds__(64 * W * G, V <= 2 ? 4 : 2) norm_grad_kernel(c
 #pragma unroll
     for (int e = 0; e < kVals; ++e) weight[j][e] = e >= slot(j).skip ? weight[j][e] : 0.f;
   }
-  u4 x[V], dy[V], res[V];
-  auto fetch = [&](int64_t row) {  // the last row again past it
-    row = row < N.rows ? row : N.rows - 1;
-    const char* const px = static_cast<const char*>(N.x.p) + row * N.x.ld * kElem;
-    const char* const pd = static_cast<const char*>(N.dy.p) + row * N.dy.ld * kElem;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      x[j] = slot(j).load(px);
-      dy[j] = slot(j).load(pd);
-    }
-    if (RES) {
-      const char* const pr = static_cast<const char*>(N.dresidual.p) + row * N.dresidual.ld * kElem;
-#pragma unroll
-      for (int j = 0; j < V; ++j) res[j] = slot(j).load(pr);
-    }
-  };
-  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * G + g;
-  fetch(row);
   int turn = 0;
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * G; base < N.rows; base += step, row += step, turn ^= 1) {
     const bool mine = row < N.rows;
-    const float mean = mine ? N.mean[row] : 0.f, rstd = mine ? N.rstd[row] : 0.f;
+    const float mean = next_mean, rstd = next_rstd;
     u4 x0[V], dy0[V], res0[V];
     // xhat and v of slot j, formed again where they are used: keeping them in
     // fp32 would take the registers of half the waves
@@ -299,28 +303,27 @@ __global__ void __launch_bounds__(64 * W * G, V <= 2 ? 4 : 2) norm_grad_kernel(c
   if (!N.partials) return;
   constexpr int kQuads = V * kVals / 4;
   if constexpr (G > 1) {
-    f4* const at = sums + (w * 64 + lane) * 2 * kQuads;
-#pragma unroll 1
-    for (int q = 1; q < G; ++q) {
-      __syncthreads();
-      if (g == q) {
+    constexpr int kItem = 2 * kQuads, kGroup = 64 * W * kItem;
+    f4* const at = sums + (w * 64 + lane) * kItem;
+    if (g > 0) {
 #pragma unroll
-        for (int j = 0; j < kQuads; ++j) {
-          const float *a = &dw[0][0] + 4 * j, *b = &db[0][0] + 4 * j;
-          at[j] = (f4){a[0], a[1], a[2], a[3]};
-          at[kQuads + j] = (f4){b[0], b[1], b[2], b[3]};
-        }
+      for (int j = 0; j < kQuads; ++j) {
+        const float *a = &dw[0][0] + 4 * j, *b = &db[0][0] + 4 * j;
+        at[(g - 1) * kGroup + j] = (f4){a[0], a[1], a[2], a[3]};
+        at[(g - 1) * kGroup + kQuads + j] = (f4){b[0], b[1], b[2], b[3]};
       }
-      __syncthreads();
-      if (g == 0) {
+    }
+    __syncthreads();
+    if (g == 0) {
+#pragma unroll 1
+      for (int q = 0; q < G - 1; ++q)
 #pragma unroll
         for (int j = 0; j < kQuads; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            (&dw[0][0])[4 * j + e] += at[j][e];
-            (&db[0][0])[4 * j + e] += at[kQuads + j][e];
+            (&dw[0][0])[4 * j + e] += at[q * kGroup + j][e];
+            (&db[0][0])[4 * j + e] += at[q * kGroup + kQuads + j][e];
           }
-      }
     }
   }
   if (g == 0) {
@@ -452,7 +455,7 @@ hipError_t norm_launch(const NormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-constexpr int kGradBlocks = 512;  // two for each CU
+constexpr int kGradBlocks = 256;  // one for each CU
 
 template <int DT, int V, int W, int G>
 hipError_t norm_grad_start(const NormGradArgs& a, int64_t limit, hipStream_t s, int* count) {
