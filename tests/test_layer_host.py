@@ -170,9 +170,86 @@ def test_dropout_binding_checks(host):
     assert len(host) == 4
 
 
+def test_gated_refusals(lib):
+    call = caller(lib.zero_gated_product, x=A, dt=F16, m=5, d=40, x_ld=40, wg=A, wu=A, f=7, w_ld=40, act=0, h=A, h_ld=7,
+                  gate=A, up=A, pre_ld=7)
+    refuse(call, (dict(m=-1), dict(d=-1), dict(f=-1), dict(dt=F32), dict(dt=0), dict(act=-1), dict(act=5), dict(x_ld=39),
+                  dict(w_ld=39), dict(h_ld=6), dict(pre_ld=6), dict(x=None), dict(wg=None), dict(wu=None), dict(h=None),
+                  dict(gate=None), dict(up=None), dict(x_ld=BIG), dict(w_ld=BIG), dict(h_ld=BIG), dict(pre_ld=BIG)),
+           zdp.ERR_INVALID_ARG)
+    refuse(call, (dict(x=A + 1), dict(wg=A + 1), dict(wu=A + 1), dict(h=A + 1), dict(gate=A + 1), dict(up=A + 1)),
+           zdp.ERR_ALIGNMENT)
+    refuse(call, (dict(m=2 ** 31), dict(f=2 ** 31, h_ld=2 ** 31, pre_ld=2 ** 31), dict(d=2 ** 31, x_ld=2 ** 31, w_ld=2 ** 31),
+                  dict(x_ld=4_194_304), dict(w_ld=4_194_304)), zdp.ERR_UNSUPPORTED)
+    assert call(m=0, x=None, h=None, gate=None, up=None) == zdp.OK
+    assert call(f=0, wg=None, wu=None, h=None, gate=None, up=None) == zdp.OK
+
+
+def test_gated_backward_refusals(lib):
+    ws = zdp.workspace_bytes(1)
+    call = caller(lib.zero_gated_product_backward, dh=A, dh_ld=7, x=A, dt=BF16, m=5, d=40, x_ld=40, wg=A, wu=A, f=7, w_ld=40,
+                  act=0, gate=A, up=A, pre_ld=7, dgate=A, dup=A, dpre_ld=7, dx=A, dx_ld=40, dwg=A, dwu=A, dw_ld=40,
+                  dw_dt=F32, accumulate=0, ws=A, ws_bytes=ws)
+    refuse(call, (dict(m=-1), dict(d=-1), dict(f=-1), dict(dt=F32), dict(act=9), dict(dh_ld=6), dict(x_ld=39), dict(w_ld=39),
+                  dict(pre_ld=6), dict(dpre_ld=6), dict(dx_ld=39), dict(dw_ld=39), dict(dw_dt=F16), dict(dw_dt=0),
+                  dict(dh=None), dict(x=None), dict(wg=None), dict(wu=None), dict(gate=None), dict(up=None),
+                  dict(dgate=None), dict(dup=None), dict(dwg=None), dict(dwu=None), dict(dh_ld=BIG), dict(x_ld=BIG),
+                  dict(w_ld=BIG), dict(pre_ld=BIG), dict(dpre_ld=BIG), dict(dx_ld=BIG), dict(dw_ld=BIG)),
+           zdp.ERR_INVALID_ARG)
+    refuse(call, (dict(dh=A + 1), dict(x=A + 1), dict(wg=A + 1), dict(wu=A + 1), dict(gate=A + 1), dict(up=A + 1),
+                  dict(dgate=A + 1), dict(dup=A + 1), dict(dx=A + 1), dict(dwg=A + 2), dict(dwu=A + 2)), zdp.ERR_ALIGNMENT)
+    refuse(call, (dict(ws=None), dict(ws=A + 128), dict(ws_bytes=ws - 1)), zdp.ERR_WORKSPACE)
+    refuse(call, (dict(m=2 ** 31), dict(x_ld=4_194_304), dict(w_ld=4_194_304), dict(dpre_ld=4_194_304)),
+           zdp.ERR_UNSUPPORTED)
+
+
+def test_gated_binding_checks(host):
+    def h16(*s):
+        return torch.zeros(*s, dtype=torch.float16)
+    x, w, h = h16(5, 8), h16(7, 8), h16(5, 7)
+    f = zdp.gated_product
+    f(x, w, w, h)
+    f(x, w, w, h, "relu", gate=h, up=h)
+    f(x[:, 1:4], w[:, :3], w[:, 2:5], h, "sigmoid")
+    assert [a[1][9] for a in host] == [0, 3, 4] and host[2][1][4] == 8
+    refused(ValueError, f, x, w, w, h, "tanh", match="act")
+    refused(TypeError, f, x.float(), w.float(), w.float(), h.float(), match="x")
+    refused(TypeError, f, x, w.bfloat16(), w, h, match="w_gate")
+    refused(TypeError, f, x, w, w.bfloat16(), h, match="w_up")
+    refused(ValueError, f, x, w, w[:6], h, match="w_up")
+    refused(ValueError, f, x, w[:, :7], w[:, :7], h, match="w_gate")
+    refused(ValueError, f, x, w, h16(7, 9)[:, :8], h, match="elements apart")
+    refused(ValueError, f, x, w, w, h[:4], match="out")
+    refused(ValueError, f, x, w, w, h, gate=h, match="together")
+    refused(ValueError, f, x, w, w, h, gate=h, up=h16(5, 8)[:, :7], match="elements apart")
+    refused(ValueError, f, x, w, w, h.t(), match="out")
+    assert len(host) == 3
+
+
+def test_gated_backward_binding_checks(host):
+    def h16(*s):
+        return torch.zeros(*s, dtype=torch.float16)
+    x, w, h, ws = h16(5, 8), h16(7, 8), h16(5, 7), torch.zeros(16, dtype=torch.uint8)
+    f = zdp.gated_product_backward
+    f(h, x, w, w, h, h, h, h, ws)
+    f(h, x, w, w, h, h, h, h, ws, dx=x, dw_gate=w.float(), dw_up=w.float(), act="gelu", accumulate=True)
+    assert host[1][1][24] is True and host[1][1][23] == F32
+    refused(ValueError, f, h, x, w, w, h, h, h, h, None, match="workspace")
+    refused(ValueError, f, h, x, w, w, h, h, h, h, ws, dw_gate=w, match="together")
+    refused(TypeError, f, h, x, w, w, h, h, h, h, ws, dw_gate=w.bfloat16(), dw_up=w.bfloat16(), match="dw_gate")
+    refused(TypeError, f, h, x, w, w, h, h, h, h, ws, dw_gate=w, dw_up=w.float(), match="dw_up")
+    refused(ValueError, f, h, x, w, w, h, h, h, h, ws, dw_gate=w, dw_up=w[:6], match="dw_up")
+    refused(ValueError, f, h, x, w, w, h, h, h, h, ws, dx=h, match="dx")
+    refused(ValueError, f, h[:4], x, w, w, h, h, h, h, ws, match="dout")
+    refused(ValueError, f, h, x, w, w, h, h[:, :6], h, h, ws, match="up")
+    refused(ValueError, f, h, x, w, w, h, h, h, h16(5, 8)[:, 1:], ws, match="elements apart")
+    refused(ValueError, f, h, x, w, w, h, h, h, h, ws, act="swish", match="act")
+    assert len(host) == 2
+
+
 def test_the_binding_passes_what_the_library_takes(lib):
     """Each call's arguments, counted: the binding gives as many as the entry point has."""
-    for name in ("layer_norm", "layer_norm_backward", "dropout"):
+    for name in ("layer_norm", "layer_norm_backward", "dropout", "gated_product", "gated_product_backward"):
         assert "stream" in inspect.signature(getattr(zdp, name)).parameters
         assert getattr(lib, f"zero_{name}").argtypes
 
