@@ -71,7 +71,8 @@ def same(got, want, what):
 SIZES = [(1, 1, 1), (1, 8, 8), (2, 7, 9), (1, 64, 64), (1, 65, 130), (3, 200, 333), (16, 64, 128), (17, 72, 136), (33, 63, 65),
          (64, 128, 64), (65, 129, 127), (63, 136, 64), (1, 1600, 640), (45, 1600, 640), (128, 256, 128), (129, 257, 255),
          (100, 1, 100), (100, 5, 77), (300, 64, 40), (257, 8, 1000), (128, 4096, 64), (5, 16, 4000), (1000, 264, 200),
-         (1001, 100, 203), (1500, 136, 1111), (70, 64, 5000), (2100, 72, 130)]
+         (1001, 100, 203), (1500, 136, 1111), (70, 64, 5000), (2100, 72, 130), (256, 2048, 3000), (250, 2043, 2995),
+         (2100, 72, 1300), (2100, 2600, 72), (2100, 2603, 70), (72, 1700, 1304), (71, 1703, 1301)]
 # many tiles of 256: forward by m x f, dx by m x d, dw by f x d
 LARGE = [(2560, 72, 2048), (2500, 67, 2001), (2561, 128, 2056), (4096, 2560, 72), (4000, 2555, 65), (4001, 2568, 136),
          (72, 2560, 2048), (67, 2555, 2043), (130, 2568, 2056), (1300, 1300, 1300)]
@@ -162,8 +163,9 @@ def close(got, want, err, what):
 
 
 def act_error(z, a):
-    """What the fp32 activation is off by, relative to a: exp's argument is rounded (|arg| u), 1 / x and the products
-    add a few u; the argument of gelu_tanh grows with z^3. Bounded by (|2 z| + 0.1 |z|^3 + 16) u of max(|a|, |z| e^-...)."""
+    """What the fp32 activation is off by: exp's argument is rounded, which is |argument| u of its value, 1 / x and the
+    products add a few u each, and the argument of gelu_tanh grows as 1.6 |z| + 0.08 |z|^3: (2 |z| + 0.1 |z|^3 + 16) u of
+    |a|. Where a falls below 2^-60 it is as good as 0 beside the products' own errors."""
     return (2 * z.abs() + 0.1 * z.abs() ** 3 + 16) * U * (a.abs() + 2.0 ** -60)
 
 

@@ -215,11 +215,11 @@ struct Operand {
 // same of wu, so that a lane holds g and u of the same outputs.
 // ------------------------------------------------------------------------
 
-template <Use USE, int FM, int FN, int WM, int WN, int kBuffers = 2>
+template <Use USE, int FM, int FN, int WM, int WN, int kBuffers = 2, int kGroups = 1>
 struct Tile {
   static constexpr int kM = kFrag * FM * WM, kN = kFrag * FN * WN;
   static constexpr int kOutN = USE == kForward ? kN / 2 : kN;  // columns of an output
-  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves * kGroups;  // waves of a group, threads of a block
   using A = Operand<kM, USE == kDw>;
   using B = Operand<kN, USE != kForward>;
   static constexpr int kPiecesA = A::kBytes / kPiece, kPiecesB = B::kBytes / kPiece;
@@ -228,7 +228,9 @@ struct Tile {
   static constexpr int kRunN = kOutN / WN;  // columns of a wave's output
   static constexpr int kOutRow = kRunN + 4;  // floats, padded
   static constexpr int kOut = kWaves * 2 * kFrag * kOutRow * 4;
-  static constexpr int kLds = kBuffers * kStage > kOut ? kBuffers * kStage : kOut;
+  static constexpr int kShared = kWaves * FM * FN * 1024;  // a group's sums
+  static constexpr int kIn = kGroups * kBuffers * kStage, kEnd = (kGroups - 1) * kShared > kOut ? (kGroups - 1) * kShared : kOut;
+  static constexpr int kLds = kIn > kEnd ? kIn : kEnd;
   static_assert(kLds <= 160 * 1024, "LDS of a CU");
   static_assert(kPiecesA % kWaves == 0 && kPiecesB % kWaves == 0, "a load's pieces belong to one operand");
 };
@@ -237,14 +239,15 @@ __device__ __forceinline__ uint32_t tiles_of(int64_t n, uint32_t size) { return 
 
 // Registers: two waves a SIMD (256 each) for the largest tile, of which one
 // block fills a CU; more blocks of the smaller ones.
-template <Use USE, Fetch FETCH, int FM, int FN, int WM, int WN, int NB, int DT, int ODT>
-__global__ void __launch_bounds__(64 * WM * WN, 2) gated_tile_kernel(const ProductArgs P) {
-  using T = Tile<USE, FM, FN, WM, WN, NB>;
+template <Use USE, Fetch FETCH, int FM, int FN, int WM, int WN, int NB, int KG, int DT, int ODT>
+__global__ void __launch_bounds__(64 * WM * WN * KG, 2) gated_tile_kernel(const ProductArgs P) {
+  using T = Tile<USE, FM, FN, WM, WN, NB, KG>;
   using A = typename T::A;
   using B = typename T::B;
   extern __shared__ __align__(1024) uint8_t lds[];
   const int lane = threadIdx.x & 63;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = KG > 1 ? wave / T::kWaves : 0, w = KG > 1 ? wave % T::kWaves : wave;
   const uint32_t tiles_m = tiles_of(P.m, T::kM), tiles_n = tiles_of(P.n, T::kOutN);
   const uint32_t rows = USE == kDw ? 2 * tiles_m : tiles_m;  // dwu's tiles behind dwg's
   const uint32_t split = P.splits > 1 ? blockIdx.x / (rows * tiles_n) : 0;
@@ -272,7 +275,9 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gated_tile_kernel(const Produ
   const uint32_t all = kParts * whole;
   const uint32_t c0 = P.splits > 1 ? static_cast<uint32_t>(static_cast<uint64_t>(all) * split / P.splits) : 0;
   const uint32_t c1 = P.splits > 1 ? static_cast<uint32_t>(static_cast<uint64_t>(all) * (split + 1) / P.splits) : all;
-  const uint32_t stages = c1 - c0;
+  // Each of the block's groups takes as many chunks; those that do not divide
+  // stand first and go to group 0, one by one.
+  const uint32_t loose = (c1 - c0) % KG, stages = (c1 - c0) / KG, first = c0 + loose + group * stages;
 
   // Load j of a wave: a piece of A (j < kLoadsA) or B. Where its lanes start,
   // from the operand's first row (column) of the tile.
@@ -302,20 +307,25 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gated_tile_kernel(const Produ
     }
     off[j] = static_cast<uint32_t>(row * (is_a ? P.a_ld : P.b_ld) + slot * 16);
   }
+  // One of two uniform pointers, by arithmetic: a select may end in vector
+  // registers, and a fetch takes its base from scalar ones.
+  auto pick = [](uint32_t second, const char* p0, const char* p1) {
+    return p0 + (-static_cast<int64_t>(second) & (p1 - p0));
+  };
   // Where load j of chunk c starts.
   auto from = [&](uint32_t c, int j) -> const char* {
-    const int part = kParts == 2 && c >= whole;
+    const uint32_t part = kParts == 2 && c >= whole;
     const uint64_t at = part ? c - whole : c;
-    if (j < T::kLoadsA) return (part ? a1 : a0) + at * astep;
-    return ((USE == kForward ? weight_of(piece(j) * kPieceRows) : part) ? b1 : b0) + at * bstep;
+    if (j < T::kLoadsA) return pick(part, a0, a1) + at * astep;
+    return pick(USE == kForward ? weight_of(piece(j) * kPieceRows) : part, b0, b1) + at * bstep;
   };
   // The lane's 16 bytes of load j of a chunk that is not whole, or of an operand
   // smaller than the tile: what does not exist is zero.
-  auto masked = [&](int part, uint32_t at, int j) -> u4 {
+  auto masked = [&](uint32_t part, uint32_t at, int j) -> u4 {
     const bool is_a = j < T::kLoadsA, cols = is_a ? USE == kDw : USE != kForward;
     const int line = is_a ? A::line(piece(j), lane) : B::line(piece(j), lane);
     const int slot = is_a ? A::slot(piece(j), lane) : B::slot(piece(j), lane);
-    const char* base = is_a ? (part ? a1 : a0) : ((USE == kForward ? weight_of(piece(j) * kPieceRows) : part) ? b1 : b0);
+    const char* base = is_a ? pick(part, a0, a1) : pick(USE == kForward ? weight_of(piece(j) * kPieceRows) : part, b0, b1);
     base += static_cast<uint64_t>(at) * (is_a ? astep : bstep) + off[j];
     const int64_t k0 = static_cast<int64_t>(at) * kChunk;
     int64_t left;
@@ -325,12 +335,13 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gated_tile_kernel(const Produ
     if (left > 0) x = load_part<DT>(base, left);
     return x;
   };
+  uint8_t* const space = lds + group * (FETCH == kDirect ? NB : 2) * T::kStage;  // the group's
   auto put = [&](int buffer, int j, u4 x) {
-    *reinterpret_cast<u4*>(lds + buffer * T::kStage + (j < T::kLoadsA ? 0 : A::kBytes) + piece(j) * kPiece + lane * 16) = x;
+    *reinterpret_cast<u4*>(space + buffer * T::kStage + (j < T::kLoadsA ? 0 : A::kBytes) + piece(j) * kPiece + lane * 16) = x;
   };
 
   const int wm = w / WN, wn = w % WN;
-  const uint32_t lds0 = lds_address(lds);
+  const uint32_t lds0 = lds_address(space);
   uint32_t aat[FM], bat[FN];
 #pragma unroll
   for (int f = 0; f < FM; ++f) aat[f] = lds0 + A::fragment((wm * FM + f) * kFrag, lane);
@@ -359,26 +370,35 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gated_tile_kernel(const Produ
     acc[x][y] = mfma<DT>(bv, av, acc[x][y]);
   };
 
-  // What is left behind the whole chunks, one run after the other.
-  if (FETCH != kMasked && rest && split == 0) {
+  // What is left behind the whole chunks, one run after the other, and the loose chunks.
+  const int rests = FETCH != kMasked && rest && split == 0 ? kParts : 0;
+  if (KG > 1 ? rests + static_cast<int>(loose) > 0 : rests > 0) {
 #pragma unroll 1
-    for (int part = 0; part < kParts; ++part) {
-      u4 x[T::kLoads];
+    for (int q = 0; q < rests + (KG > 1 ? static_cast<int>(loose) : 0); ++q) {
+      if (q) __syncthreads();  // read out
+      if (group == 0) {
+        const bool is_rest = KG == 1 || q < rests;
+        const uint32_t c = c0 + q - rests;
+        const uint32_t part = is_rest ? q : kParts == 2 && c >= whole;
+        const uint32_t at = is_rest ? whole : (part ? c - whole : c);
+        u4 x[T::kLoads];
 #pragma unroll
-      for (int j = 0; j < T::kLoads; ++j) x[j] = masked(part, whole, j);
-      if (part) __syncthreads();  // read out
+        for (int j = 0; j < T::kLoads; ++j) x[j] = masked(part, at, j);
 #pragma unroll
-      for (int j = 0; j < T::kLoads; ++j) put(1, j, x[j]);
+        for (int j = 0; j < T::kLoads; ++j) put(1, j, x[j]);
+      }
       __syncthreads();
+      if (group == 0) {
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
+        for (int s = 0; s < kSteps; ++s) {
 #pragma unroll
-        for (int k = 0; k < kKept; ++k) read_kept(1, s, k);
+          for (int k = 0; k < kKept; ++k) read_kept(1, s, k);
 #pragma unroll
-        for (int r = 0; r < kRing; ++r) {
-          read_ring(1, s, r);
+          for (int r = 0; r < kRing; ++r) {
+            read_ring(1, s, r);
 #pragma unroll
-          for (int k = 0; k < kKept; ++k) product(s, r, k);
+            for (int k = 0; k < kKept; ++k) product(s, r, k);
+          }
         }
       }
     }
@@ -397,11 +417,11 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gated_tile_kernel(const Produ
     };
     auto fetch = [&](uint32_t i, int j, uint32_t to) {
       if constexpr (FETCH == kDirect) {
-        const uint32_t c = c0 + i;
+        const uint32_t c = first + i;
         fetch_to_lds_if(i, stages, from(c, j), off[j],
                         lds0 + to * T::kStage + (j < T::kLoadsA ? 0 : A::kBytes) + piece(j) * kPiece);
       } else {
-        const uint32_t c = c0 + (i < stages ? i : stages - 1);
+        const uint32_t c = first + (i < stages ? i : stages - 1);
         if constexpr (FETCH == kStaged) pend[j] = load_any(from(c, j) + off[j]);
         else pend[j] = masked(kParts == 2 && c >= whole, kParts == 2 && c >= whole ? c - whole : c, j);
       }
@@ -484,6 +504,29 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) gated_tile_kernel(const Produ
       buffer = buffer_of(1);
     } while (++i < stages);
     __syncthreads();
+  }
+
+  // The other groups' sums, added in their order.
+  if constexpr (KG > 1) {
+    f4* const shared = reinterpret_cast<f4*>(lds) + w * FM * FN * 64 + lane;
+    constexpr int kEach = T::kShared / 16;
+    if (group > 0) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) shared[(group - 1) * kEach + (i * FN + j) * 64] = acc[i][j];
+    }
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll 1
+      for (int q = 0; q < KG - 1; ++q)
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) acc[i][j] += shared[q * kEach + (i * FN + j) * 64];
+    }
+    __syncthreads();  // the rows below go through the same LDS
+    if (group > 0) return;
   }
 
   // 32 rows of the wave's part of the tile at a time, through LDS, so that a row
@@ -730,10 +773,10 @@ __global__ void __launch_bounds__(256) gate_grad_kernel(const GateGradArgs G, in
 // Launches
 // ------------------------------------------------------------------------
 
-template <Use USE, Fetch FETCH, int FM, int FN, int WM, int WN, int NB, int DT, int ODT>
+template <Use USE, Fetch FETCH, int FM, int FN, int WM, int WN, int NB, int KG, int DT, int ODT>
 hipError_t tile_launch(const ProductArgs& a, hipStream_t s) {
-  using T = Tile<USE, FM, FN, WM, WN, NB>;
-  const auto kernel = gated_tile_kernel<USE, FETCH, FM, FN, WM, WN, NB, DT, ODT>;
+  using T = Tile<USE, FM, FN, WM, WN, NB, KG>;
+  const auto kernel = gated_tile_kernel<USE, FETCH, FM, FN, WM, WN, NB, KG, DT, ODT>;
   const int64_t tiles = ceil_div(a.m, T::kM) * ceil_div(a.n, T::kOutN) * (USE == kDw ? 2 : 1);
   if (tiles > INT32_MAX / T::kThreads / (a.splits > 1 ? a.splits : 1)) return hipErrorInvalidConfiguration;
   // more than the default limit of 64 KiB of dynamic LDS, granted once per kernel and device
@@ -756,23 +799,25 @@ bool aligned16(const void* p, int64_t ld_bytes) { return ((reinterpret_cast<uint
 
 constexpr int64_t kEnoughTiles = 160;
 constexpr int64_t kCus = 256;
+constexpr int64_t kMostCus = 208;
 constexpr int64_t kFewSmall = 448;
+constexpr int64_t kVeryFew = 128;
 
 // One tile shape with the fetch that the operands allow; fetches that write LDS
 // themselves keep NB - 1 stages in flight.
-template <Use USE, int FM, int FN, int WM, int WN, int NB, int DT, int ODT>
+template <Use USE, int FM, int FN, int WM, int WN, int NB, int KG, int DT, int ODT>
 hipError_t fetch_launch(const ProductArgs& a, hipStream_t s) {
   using T = Tile<USE, FM, FN, WM, WN>;
   if constexpr (T::kM == 64 && USE != kForward) {
-    if ((USE == kDw && a.m < T::kM) || a.n < T::kN) return tile_launch<USE, kMasked, FM, FN, WM, WN, 2, DT, ODT>(a, s);
+    if ((USE == kDw && a.m < T::kM) || a.n < T::kN) return tile_launch<USE, kMasked, FM, FN, WM, WN, 2, KG, DT, ODT>(a, s);
   }
   // a moved tile starts at n - kN: on 16 bytes if n is
   bool direct = aligned16(a.a[0], a.a_ld) && aligned16(a.b[0], a.b_ld) && (!a.a[1] || aligned16(a.a[1], a.a_ld)) &&
                 (!a.b[1] || aligned16(a.b[1], a.b_ld));
   if (USE == kDw) direct = direct && a.m % 8 == 0;
   if (USE != kForward) direct = direct && a.n % 8 == 0;
-  if (direct) return tile_launch<USE, kDirect, FM, FN, WM, WN, NB, DT, ODT>(a, s);
-  return tile_launch<USE, kStaged, FM, FN, WM, WN, 2, DT, ODT>(a, s);
+  if (direct) return tile_launch<USE, kDirect, FM, FN, WM, WN, NB, KG, DT, ODT>(a, s);
+  return tile_launch<USE, kStaged, FM, FN, WM, WN, 2, KG, DT, ODT>(a, s);
 }
 
 template <Use USE, int DT, int ODT>
@@ -795,19 +840,30 @@ hipError_t product_launch(ProductArgs a, float* scratch, hipStream_t s) {
   };
   a.splits = 1;
   a.partial = nullptr;
-  if (fits(256) && tiles(256, 256 / kHalf) >= kEnoughTiles) {
-    if constexpr (USE == kForward) return fetch_launch<USE, 4, 8, 4, 2, 2, DT, ODT>(a, s);
-    else return fetch_launch<USE, 8, 4, 2, 4, 2, DT, ODT>(a, s);
+  // By rounds over the CUs: a round of one 256 x 256 tile a CU takes as long as 1.5
+  // rounds of two 128 x 128 tiles a CU, and a round of one of those half of that.
+  // (us, large and middle tiles: forward of 1001 x 1600 x 6400, 200 and 800 tiles: 40,
+  // 50; of 2048 x 4096 x 14336, 896 and 3584: 413, 494; dx of 2048 x 4096 x 14336, 128
+  // and 512: 640, 479.)
+  const int64_t large = ceil_div(tiles(256, 256 / kHalf), kCus) * 6, pairs = ceil_div(tiles(128, 128 / kHalf), 2 * kCus) * 4;
+  if (fits(256) && (!fits(128) || large <= (tiles(128, 128 / kHalf) <= kCus ? 2 : pairs))) {
+    if constexpr (USE == kForward) return fetch_launch<USE, 4, 8, 4, 2, 2, 1, DT, ODT>(a, s);
+    else return fetch_launch<USE, 8, 4, 2, 4, 2, 1, DT, ODT>(a, s);
   }
-  const bool middle = fits(128) && tiles(128, 128 / kHalf) >= kEnoughTiles;
+  const int64_t mid = tiles(128, 128 / kHalf);
+  bool middle = fits(128) && mid >= kEnoughTiles;
   if constexpr (USE != kForward) {
-    // few tiles over a long contraction: shared among blocks, as far as the scratch holds their sums
-    const int64_t have = middle ? tiles(128, 128) : tiles(64, 128);
+    // Few tiles over a long contraction are shared among blocks, as far as the
+    // scratch holds their sums: middle tiles where that gives nearly every CU one (dx
+    // of 256 x 4096 x 14336, 64 tiles in 4 splits: 123 us with small tiles, 87; of 300
+    // rows, 96 in 2: 140 and 159), else small ones, two blocks a CU.
     const int64_t chunks = ceil_div(a.k, kChunk) * (USE == kDx ? 2 : 1);
-    int64_t splits = 512 / have;
-    splits = splits < chunks / 4 ? splits : chunks / 4;
     const int64_t room = static_cast<int64_t>(kScratchBytes / sizeof(float)) / (a.m * a.n * kOutputs);
-    splits = splits < room ? splits : room;
+    const int64_t most = room < chunks / 4 ? room : chunks / 4;
+    auto shared = [&](int64_t have, int64_t want) { return want / have < most ? want / have : most; };
+    const int64_t one = fits(128) ? shared(mid, kCus) : 0;
+    middle = middle || mid * one > kMostCus;
+    const int64_t splits = middle ? (mid >= kEnoughTiles ? shared(mid, 2 * kCus) : one) : shared(tiles(64, 128), 2 * kCus);
     if (splits > 1) {
       a.splits = static_cast<int32_t>(splits);
       a.partial = scratch;
@@ -818,15 +874,19 @@ hipError_t product_launch(ProductArgs a, float* scratch, hipStream_t s) {
   // flight; where there are two a CU, four waves and one stage each are as good (dx
   // of 2000 x 2048 x 8000, 256 tiles: 215 us with four waves, 203 with eight, 138
   // with three stages in flight too; forward of 128 x 4096 x 14336, 224: 74, 70, 58).
+  // Very few small tiles of a forward pass, which has no scratch to split over, are
+  // halved, and two groups of waves share the contraction (16 x 8192 x 2048: 47 -> 26.5
+  // us; 64 x 4096 x 4096: 26 -> 17; 64 x 4096 x 14336, 224 tiles: 52.5 against 60).
   // The small tile has two stages in flight where its blocks do not fill the CUs
   // (forward of 17 x 4096 x 14336, 224 blocks: 61 -> 47.5 us; dx of 1001 x 1600 x
   // 6400, 416: 74 -> 65) and one where they do (dx of 16 x 4096 x 14336, 512: 46.5
   // against 50).
   const int64_t blocks = (middle ? tiles(128, 128 / kHalf) : tiles(64, 128 / kHalf)) * a.splits;
-  if (middle && blocks <= kCus) e = fetch_launch<USE, 2, 4, 4, 2, 4, DT, ODT>(a, s);
-  else if (middle) e = fetch_launch<USE, 4, 4, 2, 2, 2, DT, ODT>(a, s);
-  else if (blocks <= kFewSmall) e = fetch_launch<USE, 2, 4, 2, 2, 3, DT, ODT>(a, s);
-  else e = fetch_launch<USE, 2, 4, 2, 2, 2, DT, ODT>(a, s);
+  if (middle && blocks <= kCus) e = fetch_launch<USE, 2, 4, 4, 2, 4, 1, DT, ODT>(a, s);
+  else if (middle) e = fetch_launch<USE, 4, 4, 2, 2, 2, 1, DT, ODT>(a, s);
+  else if (USE == kForward && blocks <= kVeryFew) e = fetch_launch<USE, 4, 2, 1, 2, 4, 2, DT, ODT>(a, s);
+  else if (blocks <= kFewSmall) e = fetch_launch<USE, 2, 4, 2, 2, 3, 1, DT, ODT>(a, s);
+  else e = fetch_launch<USE, 2, 4, 2, 2, 2, 1, DT, ODT>(a, s);
   if (e != hipSuccess || a.splits <= 1) return e;
   const int64_t join = ceil_div(a.m * a.n, 256);
   hipLaunchKernelGGL((gated_join_kernel<ODT>), dim3(static_cast<uint32_t>(join < 4096 ? join : 4096), kOutputs), dim3(256),
