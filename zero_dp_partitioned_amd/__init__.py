@@ -795,11 +795,16 @@ def mx_product(a_codes, a_scales, b_codes, b_scales, out, stream=None):
 # distance from row to row; see include/zero_dp.h
 # --------------------------------------------------------------------------
 
-def _like(t, name, dtypes, device, rows, cols):
-    """The elements from row to row of a 2-D tensor of the given shape."""
+def _like(t, name, dtypes, device, shape):
+    """The elements from row to row of a 2-D tensor of the given shape (a torch.Size)."""
+    try:  # the common case in few look-ups: dense, and nothing wrong
+        if t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == device:
+            return shape[1]
+    except (AttributeError, TypeError):
+        pass  # what follows says what is wrong
     r, c, ld = _need_rows(t, name, dtypes, device)
-    if r != rows or c != cols:
-        raise ValueError(f"{name}: {r} x {c}, expected {rows} x {cols}")
+    if (r, c) != tuple(shape):
+        raise ValueError(f"{name}: {r} x {c}, expected {shape[0]} x {shape[1]}")
     return ld
 
 
@@ -834,7 +839,7 @@ def layer_norm(x, weight, bias, y, eps=1e-5, mean=None, rstd=None, stream=None):
     dev = _device_of(x, "x")
     types, f32 = _mx_types(), (_mx().f32,)
     rows, cols, x_ld = _need_rows(x, "x", types, dev)
-    y_ld = _like(y, "y", (x.dtype,), dev, rows, cols)
+    y_ld = _like(y, "y", (x.dtype,), dev, x.shape)
     w, w_dt = _weight(weight, dev, x.dtype, cols)
     b = _vector(bias, "bias", (weight.dtype,), dev, cols)
     if (mean is None) != (rstd is None):
@@ -853,11 +858,11 @@ def layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None,
     types, f32 = _mx_types(), (_mx().f32,)
     rows, cols, x_ld = _need_rows(x, "x", types, dev)
     one = (x.dtype,)
-    dy_ld, dx_ld = _like(dy, "dy", one, dev, rows, cols), _like(dx, "dx", one, dev, rows, cols)
+    dy_ld, dx_ld = _like(dy, "dy", one, dev, x.shape), _like(dx, "dx", one, dev, x.shape)
     w, w_dt = _weight(weight, dev, x.dtype, cols)
     if mean is None or rstd is None:
         raise TypeError("mean and rstd are needed (from layer_norm)")
-    res_ld = 0 if dresidual is None else _like(dresidual, "dresidual", one, dev, rows, cols)
+    res_ld = 0 if dresidual is None else _like(dresidual, "dresidual", one, dev, x.shape)
     dw, db = _vector(dweight, "dweight", types, dev, cols), None
     if dbias is not None:
         db = _vector(dbias, "dbias", types if dweight is None else (dweight.dtype,), dev, cols)
@@ -878,27 +883,27 @@ def dropout(x, y, p, seed, offset=0, residual=None, first=0, counter=None, strea
     that is added to offset when the kernel runs. y may be x or residual."""
     dev = _device_of(x, "x")
     types = _mx_types()
-    flat = x.dim() != 2
-    shape = x.shape
+    shape, one = x.shape, (x.dtype,)
+    flat = len(shape) != 2
 
-    def rows_of(t, name):
+    def ld_of(t, name):
+        if not flat:
+            return _like(t, name, one, dev, shape)
+        n = _need_values(t, name, one, dev)
         if t.shape != shape:
             raise ValueError(f"{name}: {tuple(t.shape)}, expected {tuple(shape)}")
-        if flat:
-            return _need_values(t, name, (x.dtype,), dev)
-        return _need_rows(t, name, (x.dtype,), dev)[2]
+        return n
 
     if flat:
-        n = _need_values(x, "x", types, dev)
-        rows, cols, x_ld = 1, n, n
+        cols = x_ld = _need_values(x, "x", types, dev)
+        rows = 1
     else:
         rows, cols, x_ld = _need_rows(x, "x", types, dev)
-    if not isinstance(y, _mx().tensor):
-        raise TypeError(f"y: a torch tensor is expected, got {type(y).__name__}")
-    y_ld = rows_of(y, "y")
+    y_ld = ld_of(y, "y")
     res, res_ld = None, 0
     if residual is not None:
-        res, res_ld = residual.data_ptr(), rows_of(residual, "residual")
+        res_ld = ld_of(residual, "residual")
+        res = residual.data_ptr()
     if counter is not None:
         counter = _vector(counter, "counter", (_torch().int64,), dev, 1)
     mask = (1 << 64) - 1
@@ -913,16 +918,21 @@ def _activation(act):
     return code
 
 
-def _pair(first, second, names, dtypes, device, rows, cols):
+def _pair(first, second, names, dtypes, device, shape):
     """The elements from row to row of two tensors of one type, shape and row distance."""
-    ld = _like(first, names[0], dtypes, device, rows, cols)
-    if _like(second, names[1], (first.dtype,), device, rows, cols) != ld:
+    ld = _like(first, names[0], dtypes, device, shape)
+    if _like(second, names[1], (first.dtype,), device, shape) != ld:
         raise ValueError(f"{names[0]} and {names[1]}: rows lie {ld} and {second.stride(0)} elements apart")
     return ld
 
 
+_HALF_TYPES = {}
+
+
 def _half_types():
-    return {t: c for t, c in _mx_types().items() if c != DT_F32}
+    if not _HALF_TYPES:
+        _HALF_TYPES.update({t: c for t, c in _mx_types().items() if c != DT_F32})
+    return _HALF_TYPES
 
 
 def gated_product(x, w_gate, w_up, out, act="silu", gate=None, up=None, stream=None):
@@ -936,15 +946,19 @@ def gated_product(x, w_gate, w_up, out, act="silu", gate=None, up=None, stream=N
     types = _half_types()
     m, d, x_ld = _need_rows(x, "x", types, dev)
     one = (x.dtype,)
-    f = _need_rows(w_gate, "w_gate", one, dev)[0]
-    w_ld = _pair(w_gate, w_up, ("w_gate", "w_up"), one, dev, f, d)
-    h_ld = _like(out, "out", one, dev, m, f)
+    f, d_w, w_ld = _need_rows(w_gate, "w_gate", one, dev)
+    if d_w != d:
+        raise ValueError(f"w_gate: {f} x {d_w}, expected rows of {d}")
+    if _like(w_up, "w_up", one, dev, w_gate.shape) != w_ld:
+        raise ValueError(f"w_gate and w_up: rows lie {w_ld} and {w_up.stride(0)} elements apart")
+    m_f = _torch().Size((m, f))
+    h_ld = _like(out, "out", one, dev, m_f)
     if (gate is None) != (up is None):
         raise ValueError("gate and up must be given together")
     g = u = None
     pre_ld = 0
     if gate is not None:
-        pre_ld = _pair(gate, up, ("gate", "up"), one, dev, m, f)
+        pre_ld = _pair(gate, up, ("gate", "up"), one, dev, m_f)
         g, u = gate.data_ptr(), up.data_ptr()
     _call(load().zero_gated_product, dev, stream, x.data_ptr(), types[x.dtype], m, d, x_ld, w_gate.data_ptr(),
           w_up.data_ptr(), f, w_ld, _activation(act), out.data_ptr(), h_ld, g, u, pre_ld)
@@ -962,21 +976,25 @@ def gated_product_backward(dout, x, w_gate, w_up, gate, up, dgate, dup, workspac
     types = _half_types()
     m, d, x_ld = _need_rows(x, "x", types, dev)
     one = (x.dtype,)
-    f = _need_rows(w_gate, "w_gate", one, dev)[0]
-    w_ld = _pair(w_gate, w_up, ("w_gate", "w_up"), one, dev, f, d)
-    dh_ld = _like(dout, "dout", one, dev, m, f)
-    pre_ld = _pair(gate, up, ("gate", "up"), one, dev, m, f)
-    dpre_ld = _pair(dgate, dup, ("dgate", "dup"), one, dev, m, f)
+    f, d_w, w_ld = _need_rows(w_gate, "w_gate", one, dev)
+    if d_w != d:
+        raise ValueError(f"w_gate: {f} x {d_w}, expected rows of {d}")
+    if _like(w_up, "w_up", one, dev, w_gate.shape) != w_ld:
+        raise ValueError(f"w_gate and w_up: rows lie {w_ld} and {w_up.stride(0)} elements apart")
+    m_f = _torch().Size((m, f))
+    dh_ld = _like(dout, "dout", one, dev, m_f)
+    pre_ld = _pair(gate, up, ("gate", "up"), one, dev, m_f)
+    dpre_ld = _pair(dgate, dup, ("dgate", "dup"), one, dev, m_f)
     ws, ws_bytes = _scratch(workspace, dev)
     dx_p, dx_ld = None, 0
     if dx is not None:
-        dx_p, dx_ld = dx.data_ptr(), _like(dx, "dx", one, dev, m, d)
+        dx_p, dx_ld = dx.data_ptr(), _like(dx, "dx", one, dev, x.shape)
     if (dw_gate is None) != (dw_up is None):
         raise ValueError("dw_gate and dw_up must be given together")
     dg = du = None
     dw_ld = dw_dt = 0
     if dw_gate is not None:
-        dw_ld = _pair(dw_gate, dw_up, ("dw_gate", "dw_up"), (x.dtype, _mx().f32), dev, f, d)
+        dw_ld = _pair(dw_gate, dw_up, ("dw_gate", "dw_up"), (x.dtype, _mx().f32), dev, w_gate.shape)
         dg, du, dw_dt = dw_gate.data_ptr(), dw_up.data_ptr(), _mx_types()[dw_gate.dtype]
     _call(load().zero_gated_product_backward, dev, stream, dout.data_ptr(), dh_ld, x.data_ptr(), types[x.dtype], m, d,
           x_ld, w_gate.data_ptr(), w_up.data_ptr(), f, w_ld, _activation(act), gate.data_ptr(), up.data_ptr(), pre_ld,
