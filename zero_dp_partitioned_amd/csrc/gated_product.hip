@@ -450,8 +450,8 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) gated_tile_kernel(const 
     // fragments have been asked for (group kTurn), the next stage is published,
     // and what follows is read from there; the fetches of the stage after it
     // start into this stage's place, one a group, and run on into the next
-    // stage's first step. Stages that pass through registers are fetched in their
-    // predecessor's first step.
+    // stage's first step; those that pass through registers, which publishing has
+    // just emptied, at the same time.
     constexpr int kTurn = kRing - kAhead;
     auto step = [&](auto sc, uint32_t i) {
       constexpr int S = decltype(sc)::value;
@@ -459,18 +459,12 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) gated_tile_kernel(const 
 #pragma unroll
       for (int t = 0; t < kRing; ++t) {
         if (kLast && t == kTurn) publish(i + 1, buffer_of(1));
-        if constexpr (FETCH == kDirect) {
-          constexpr int kEach = (T::kLoads + kRing - 1) / kRing;
-          const int slot = kLast ? t - kTurn : kAhead + S * kRing + t;
+        constexpr int kEach = (T::kLoads + kRing - 1) / kRing;
+        const int slot = kLast ? t - kTurn : kAhead + S * kRing + t;
 #pragma unroll
-          for (int q = 0; q < kEach; ++q)
-            if (slot >= 0 && slot * kEach + q < T::kLoads) fetch(i + kBuffers - (kLast ? 0 : 1), slot * kEach + q, kLast ? buffer : buffer_of(kBuffers - 1));
-        } else if constexpr (S == 0) {
-          constexpr int kEach = (T::kLoads + kRing - 1) / kRing;
-#pragma unroll
-          for (int q = 0; q < kEach; ++q)
-            if (t * kEach + q < T::kLoads) fetch(i + 1, t * kEach + q, 0);
-        }
+        for (int q = 0; q < kEach; ++q)
+          if (slot >= 0 && slot * kEach + q < T::kLoads)
+            fetch(i + kBuffers - (kLast ? 0 : 1), slot * kEach + q, kLast ? buffer : buffer_of(kBuffers - 1));
 #pragma unroll
         for (int k = 0; k < kKept; ++k) product(S, t, k);
         const bool next = kLast && t >= kTurn;  // the next stage's
@@ -491,12 +485,9 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) gated_tile_kernel(const 
     for (int k = 0; k < kKept; ++k) read_kept(0, 0, k);
 #pragma unroll
     for (int r = 0; r < kAhead; ++r) read_ring(0, 0, r);
-    if constexpr (FETCH == kDirect) {
-      constexpr int kEach = (T::kLoads + kRing - 1) / kRing;
-      constexpr int kEarly = kAhead * kEach < T::kLoads ? kAhead * kEach : T::kLoads;
+    constexpr int kEarly = kAhead * ((T::kLoads + kRing - 1) / kRing);
 #pragma unroll
-      for (int j = 0; j < kEarly; ++j) fetch(kBuffers - 1, j, kBuffers - 1);
-    }
+    for (int j = 0; j < (kEarly < T::kLoads ? kEarly : T::kLoads); ++j) fetch(kBuffers - 1, j, kBuffers - 1);
     uint32_t i = 0;
     do {
       step(std::integral_constant<int, 0>{}, i);
@@ -882,9 +873,11 @@ hipError_t product_launch(ProductArgs a, float* scratch, hipStream_t s) {
   // 6400, 416: 74 -> 65) and one where they do (dx of 16 x 4096 x 14336, 512: 46.5
   // against 50).
   const int64_t blocks = (middle ? tiles(128, 128 / kHalf) : tiles(64, 128 / kHalf)) * a.splits;
+  if constexpr (USE == kForward) {
+    if (!middle && blocks <= kVeryFew) return fetch_launch<USE, 4, 2, 1, 2, 4, 2, DT, ODT>(a, s);
+  }
   if (middle && blocks <= kCus) e = fetch_launch<USE, 2, 4, 4, 2, 4, 1, DT, ODT>(a, s);
   else if (middle) e = fetch_launch<USE, 4, 4, 2, 2, 2, 1, DT, ODT>(a, s);
-  else if (USE == kForward && blocks <= kVeryFew) e = fetch_launch<USE, 4, 2, 1, 2, 4, 2, DT, ODT>(a, s);
   else if (blocks <= kFewSmall) e = fetch_launch<USE, 2, 4, 2, 2, 3, 1, DT, ODT>(a, s);
   else e = fetch_launch<USE, 2, 4, 2, 2, 2, 1, DT, ODT>(a, s);
   if (e != hipSuccess || a.splits <= 1) return e;
