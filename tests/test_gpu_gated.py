@@ -288,6 +288,21 @@ def test_one_row_s_trouble_stays_its_own(m, ws):
     assert torch.equal(~dwg.isfinite(), bad) and torch.equal(~dwu.isfinite(), bad)
 
 
+@pytest.mark.parametrize("m", [1, 2, 4])
+@pytest.mark.parametrize("d", [9, 520, 1029])
+def test_infinite_weights_of_single_tokens(m, d):
+    """An infinite weight makes its own outputs infinite, with no NaN from the values that lanes past the end load again."""
+    x = torch.ones(m, d, dtype=torch.bfloat16, device=DEV)
+    wg, wu = torch.ones(20, d, dtype=torch.bfloat16, device=DEV), torch.ones(20, d, dtype=torch.bfloat16, device=DEV)
+    wg[3, d - 1] = wg[4, d - 8] = wg[5, 0] = float("inf")
+    h, g, u = (torch.empty(m, 20, dtype=torch.bfloat16, device=DEV) for _ in range(3))
+    zdp.gated_product(x, wg, wu, h, "relu", gate=g, up=u)
+    want = torch.full((m, 20), float(d), device=DEV).bfloat16()
+    assert torch.equal(u, want)
+    want[:, 3:6] = float("inf")
+    assert torch.equal(g, want) and h[:, 3:6].isinf().all() and h[:, 6:].isfinite().all()
+
+
 def test_results_repeat(ws):
     """No atomics: the same call gives the same bits."""
     g = torch.Generator(device=DEV).manual_seed(5)

@@ -253,6 +253,29 @@ def test_operands_whose_rows_lie_as_far_apart_as_they_may(ld):
     assert all(torch.equal(p, q) for p, q in zip(near, run(x, wg, wu, dg, du)))
 
 
+def test_a_large_tile_s_rows_as_far_apart_as_they_may():
+    """256 rows of a tile, 2^31 bytes from the first to the last, in the forward pass and in dx."""
+    m, d, f, ld = 2560, 72, 2048, 4_194_296
+    g = torch.Generator(device=DEV).manual_seed(2)
+    x, wg, wu = (torch.randn(*s, generator=g, device=DEV).half() for s in ((m, d), (f, d), (f, d)))
+    big = torch.zeros((m - 1) * ld + m, dtype=x.dtype, device=DEV)
+    near, far = torch.empty(m, f, dtype=x.dtype, device=DEV), torch.empty(m, f, dtype=x.dtype, device=DEV)
+    zdp.gated_product(x, wg, wu, near)
+    spread = big.as_strided((m, d), (ld, 1))
+    spread.copy_(x)
+    zdp.gated_product(spread, wg, wu, far)
+    assert torch.equal(near, far)
+    # dx of 2560 x 2560 from dgate and dup with 72 columns, far apart
+    dh, gate = (torch.randn(m, d, generator=g, device=DEV).half() for _ in range(2))
+    w = torch.randn(d, m, generator=g, device=DEV).half()
+    xx, ws = torch.zeros(m, m, dtype=x.dtype, device=DEV), zdp.new_workspace(1)
+    a, b = torch.empty_like(xx), torch.empty_like(xx)
+    zdp.gated_product_backward(dh, xx, w, w, gate, gate, torch.empty_like(dh), torch.empty_like(dh), ws, dx=a)
+    du = torch.zeros_like(big).as_strided((m, d), (ld, 1))
+    zdp.gated_product_backward(dh, xx, w, w, gate, gate, spread, du, ws, dx=b)
+    assert torch.equal(a, b)
+
+
 def test_refusals_on_the_device():
     x, w, v = torch.zeros(4, 64, device=DEV).half(), torch.zeros(8, 64, device=DEV).half(), torch.zeros(64, device=DEV)
     h, ws = torch.zeros(4, 8, device=DEV).half(), zdp.new_workspace(1)

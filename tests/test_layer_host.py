@@ -165,6 +165,8 @@ def test_dropout_binding_checks(host):
     refused(ValueError, f, x, x, 0.5, 1, residual=x[:, :7], match="residual")
     refused(ValueError, f, x.t(), x, 0.5, 1)
     refused(ValueError, f, x.view(2, 2, 8)[:, :, :4], torch.zeros(2, 2, 4), 0.5, 1, match="contiguous")
+    refused(ValueError, f, x, x, 0.5, 1, first=2 ** 64, match="first")  # would wrap to 0
+    refused(ValueError, f, x, x, 0.5, 1, first=-1, match="first")
     refused(TypeError, f, x, x, 0.5, 1, counter=torch.zeros(1), match="counter")
     refused(ValueError, f, x, x, 0.5, 1, counter=torch.zeros(2, dtype=torch.int64), match="counter")
     assert len(host) == 4

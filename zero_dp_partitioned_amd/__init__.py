@@ -906,6 +906,8 @@ def dropout(x, y, p, seed, offset=0, residual=None, first=0, counter=None, strea
         res = residual.data_ptr()
     if counter is not None:
         counter = _vector(counter, "counter", (_torch().int64,), dev, 1)
+    if not 0 <= first < 1 << 63:
+        raise ValueError(f"first = {first} is not in [0, 2^63)")
     mask = (1 << 64) - 1
     _call(load().zero_dropout, dev, stream, x.data_ptr(), types[x.dtype], rows, cols, x_ld, res, res_ld, y.data_ptr(),
           y_ld, p, seed & mask, offset & mask, counter, first)

@@ -44,6 +44,7 @@ struct ProductArgs {
   void* out[3];
   int64_t out_ld[3];
   int32_t act, accumulate;
+  bool dry;        // launch nothing, say whether a launch holds the tiles
   int32_t splits;  // blocks that share a tile's contraction, each leaving fp32 sums at `partial`
   float* partial;  // [splits][outputs][m][n]
 };
@@ -209,8 +210,9 @@ struct Operand {
 
 // ------------------------------------------------------------------------
 // The tile kernel: WM x WN waves, each with FM x FN fragments, share an output
-// tile through LDS, two stages of one chunk each. A stage is fetched while the
-// stage before is multiplied, the loads between the products. The rows of B of
+// tile through LDS in stages of one chunk, NB of them: one is multiplied while the
+// others are fetched, the loads between the products. KG groups of such waves may
+// share the contraction, each with stages of its own. The rows of B of
 // a forward tile are, wave column by wave column, FN / 2 fragments of wg and the
 // same of wu, so that a lane holds g and u of the same outputs.
 // ------------------------------------------------------------------------
@@ -239,6 +241,15 @@ __device__ __forceinline__ uint32_t tiles_of(int64_t n, uint32_t size) { return 
 
 // Registers: two waves a SIMD (256 each) for the largest tile, of which one
 // block fills a CU; more blocks of the smaller ones.
+//
+// What bounds the large tile (256 x 256, eight waves of 128 x 64 or 64 x 128) is
+// power: 8192 x 4096 x 14336 in bf16 takes 1395-1470 us (1.31-1.38 PFLOP/s), dx
+// 1340-1410, dw 1380-1430 on several cards, at 1.5-1.9 GHz; with the wait for
+// fetches left out it took 1-2 % less. The instruction alone reaches 2.08 PFLOP/s on
+// such values (32 x 32 x 16: 1.83, and the kernel was 2-3 % slower with it). Four
+// waves of 128 x 128, which read a third less from LDS, were 5 % slower for dw: one
+// wave a SIMD shows every wait. Higher priority for one wave of each SIMD, or around
+// the products, changed 1 % either way.
 template <Use USE, Fetch FETCH, int FM, int FN, int WM, int WN, int NB, int KG, int DT, int ODT>
 __global__ void __launch_bounds__(64 * WM * WN * KG, 2) gated_tile_kernel(const ProductArgs P) {
   using T = Tile<USE, FM, FN, WM, WN, NB, KG>;
@@ -647,24 +658,31 @@ __global__ void __launch_bounds__(64 * kTokenWaves) gated_token_kernel(const Pro
   const char* const wg = P.b[0] + n0 * P.b_ld;
   const char* const wu = P.b[1] + n0 * P.b_ld;
   float acc[kValues] = {};  // of product z, row r, token t at (z * 16 + r) * T + t
-  for (int64_t run = static_cast<int64_t>(w) * kTokenRun; run < P.k; run += NW * kTokenRun) {
-    // a lane past the end, or that would pass it, takes the last 8 values; what another lane has is zero in x
-    const int64_t k = run + lane * 8, at = k < P.k - 8 ? k : P.k - 8;
-    const uint32_t off = static_cast<uint32_t>((at - run) * 2);
+  // A run; the contraction's last one may end inside it. A lane that would pass the
+  // end takes the last 8 values there, and what another lane has is zero on both
+  // sides (an infinite weight times a zero of x alone would be NaN).
+  auto work = [&](auto ends, int64_t run) {
+    constexpr bool kEnds = decltype(ends)::value;
+    const int64_t k = run + lane * 8, at = !kEnds || k < P.k - 8 ? k : P.k - 8;
+    const int skip = kEnds ? static_cast<int>(k - at) : 0;
+    const int32_t off = static_cast<int32_t>((at - run) * 2);
+    auto values = [&](u4 raw, float* v) {
+      widen<DT>(raw, v);
+      if constexpr (kEnds) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = e >= skip ? v[e] : 0.f;
+      }
+    };
     float x[T][8];
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-      widen<DT>(load_any(P.a[0] + (t < P.m ? t : P.m - 1) * P.a_ld + at * 2), x[t]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[t][e] = e >= k - at ? x[t][e] : 0.f;
-    }
+    for (int t = 0; t < T; ++t) values(load_any(P.a[0] + (t < P.m ? t : P.m - 1) * P.a_ld + at * 2), x[t]);
     u4 v[2][2][kTogether];
     auto fetch = [&](int r0, u4 (&to)[2][kTogether]) {
 #pragma unroll
       for (int r = 0; r < kTogether; ++r) {
         const int64_t row = r0 + r < last ? r0 + r : last;
-        to[0][r] = load_any(wg + row * P.b_ld + run * 2 + static_cast<int32_t>(off));
-        to[1][r] = load_any(wu + row * P.b_ld + run * 2 + static_cast<int32_t>(off));
+        to[0][r] = load_any(wg + row * P.b_ld + run * 2 + off);
+        to[1][r] = load_any(wu + row * P.b_ld + run * 2 + off);
       }
     };
     fetch(0, v[0]);
@@ -678,7 +696,7 @@ __global__ void __launch_bounds__(64 * kTokenWaves) gated_token_kernel(const Pro
 #pragma unroll
         for (int r = 0; r < kTogether; ++r) {
           float y[8];
-          widen<DT>(v[now][z][r], y);
+          values(v[now][z][r], y);
 #pragma unroll
           for (int t = 0; t < T; ++t)
 #pragma unroll
@@ -689,7 +707,10 @@ __global__ void __launch_bounds__(64 * kTokenWaves) gated_token_kernel(const Pro
         }
       __builtin_amdgcn_sched_barrier(0);
     }
-  }
+  };
+  int64_t run = static_cast<int64_t>(w) * kTokenRun;
+  for (; run + kTokenRun <= P.k; run += NW * kTokenRun) work(std::false_type{}, run);
+  if (run < P.k) work(std::true_type{}, run);
   lanes_sums<kValues, 32>(acc, lane);
   constexpr int kEach = kValues >= 64 ? kValues / 64 : 1, kLanes = kValues >= 64 ? 1 : 64 / kValues;  // values a lane, lanes a value
 #pragma unroll
@@ -770,6 +791,7 @@ hipError_t tile_launch(const ProductArgs& a, hipStream_t s) {
   const auto kernel = gated_tile_kernel<USE, FETCH, FM, FN, WM, WN, NB, KG, DT, ODT>;
   const int64_t tiles = ceil_div(a.m, T::kM) * ceil_div(a.n, T::kOutN) * (USE == kDw ? 2 : 1);
   if (tiles > INT32_MAX / T::kThreads / (a.splits > 1 ? a.splits : 1)) return hipErrorInvalidConfiguration;
+  if (a.dry) return hipSuccess;
   // more than the default limit of 64 KiB of dynamic LDS, granted once per kernel and device
   static std::atomic<uint64_t> granted{0};
   int dev = 0;
@@ -815,7 +837,7 @@ template <Use USE, int DT, int ODT>
 hipError_t product_launch(ProductArgs a, float* scratch, hipStream_t s) {
   constexpr int kOutputs = USE == kDw ? 2 : 1;
   if constexpr (USE == kForward) {
-    if (a.m <= kTokens && a.k >= 8) {
+    if (a.m <= kTokens && a.k >= 8 && ceil_div(a.n, kFrag) <= INT32_MAX / (64 * kTokenWaves)) {
       const dim3 blocks(static_cast<uint32_t>(ceil_div(a.n, kFrag))), threads(64 * kTokenWaves);
       if (a.m == 1) hipLaunchKernelGGL((gated_token_kernel<1, DT>), blocks, threads, 0, s, a);
       else if (a.m == 2) hipLaunchKernelGGL((gated_token_kernel<2, DT>), blocks, threads, 0, s, a);
@@ -880,7 +902,7 @@ hipError_t product_launch(ProductArgs a, float* scratch, hipStream_t s) {
   else if (middle) e = fetch_launch<USE, 4, 4, 2, 2, 2, 1, DT, ODT>(a, s);
   else if (blocks <= kFewSmall) e = fetch_launch<USE, 2, 4, 2, 2, 3, 1, DT, ODT>(a, s);
   else e = fetch_launch<USE, 2, 4, 2, 2, 2, 1, DT, ODT>(a, s);
-  if (e != hipSuccess || a.splits <= 1) return e;
+  if (e != hipSuccess || a.splits <= 1 || a.dry) return e;
   const int64_t join = ceil_div(a.m * a.n, 256);
   hipLaunchKernelGGL((gated_join_kernel<ODT>), dim3(static_cast<uint32_t>(join < 4096 ? join : 4096), kOutputs), dim3(256),
                      0, s, a, kOutputs);
@@ -906,19 +928,9 @@ hipError_t forward_launch(const GatedArgs& g, hipStream_t s) {
 }
 
 template <int DT>
-hipError_t grad_launch(const GatedGradArgs& g, hipStream_t s) {
-  if (g.m > 0 && g.f > 0) {
-    GateGradArgs e = {g.dh, {g.pre[0], g.pre[1]}, {g.dpre[0], g.dpre[1]}, g.m, g.f, g.act};
-    if (g.dh.ld == g.f && g.pre[0].ld == g.f && g.dpre[0].ld == g.f) {  // one row
-      e.cols *= e.rows;
-      e.rows = 1;
-    }
-    const int64_t row_slots = ceil_div(e.cols, Vec<DT>::kVals), slots = row_slots * e.rows, blocks = ceil_div(slots, 256);
-    const int grid = limit_grid(static_cast<int>(blocks < kMaxGrid ? blocks : kMaxGrid));
-    hipLaunchKernelGGL((gate_grad_kernel<DT>), dim3(grid), dim3(256), 0, s, e, row_slots, slots);
-    if (hipError_t x = hipGetLastError()) return x;
-  }
+hipError_t products_of_grad(const GatedGradArgs& g, bool dry, hipStream_t s) {
   ProductArgs a = {};
+  a.dry = dry;
   if (g.dx.p && g.m > 0 && g.d > 0) {
     for (int i = 0; i < 2; ++i) {
       a.a[i] = static_cast<const char*>(g.dpre[i].p);
@@ -935,6 +947,7 @@ hipError_t grad_launch(const GatedGradArgs& g, hipStream_t s) {
   }
   if (g.dw[0].p && g.f > 0 && g.d > 0) {
     a = {};
+    a.dry = dry;
     for (int i = 0; i < 2; ++i) {
       a.a[i] = static_cast<const char*>(g.dpre[i].p);
       a.out[i] = g.dw[i].p;
@@ -951,6 +964,24 @@ hipError_t grad_launch(const GatedGradArgs& g, hipStream_t s) {
     return product_launch<kDw, DT, DT>(a, g.scratch, s);
   }
   return hipSuccess;
+}
+
+template <int DT>
+hipError_t grad_launch(const GatedGradArgs& g, hipStream_t s) {
+  // a call that cannot launch all of it launches nothing
+  if (hipError_t e = products_of_grad<DT>(g, true, s)) return e;
+  if (g.m > 0 && g.f > 0) {
+    GateGradArgs e = {g.dh, {g.pre[0], g.pre[1]}, {g.dpre[0], g.dpre[1]}, g.m, g.f, g.act};
+    if (g.dh.ld == g.f && g.pre[0].ld == g.f && g.dpre[0].ld == g.f) {  // one row
+      e.cols *= e.rows;
+      e.rows = 1;
+    }
+    const int64_t row_slots = ceil_div(e.cols, Vec<DT>::kVals), slots = row_slots * e.rows, blocks = ceil_div(slots, 256);
+    const int grid = limit_grid(static_cast<int>(blocks < kMaxGrid ? blocks : kMaxGrid));
+    hipLaunchKernelGGL((gate_grad_kernel<DT>), dim3(grid), dim3(256), 0, s, e, row_slots, slots);
+    if (hipError_t x = hipGetLastError()) return x;
+  }
+  return products_of_grad<DT>(g, false, s);
 }
 
 }  // namespace
