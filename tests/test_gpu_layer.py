@@ -184,6 +184,24 @@ def test_norm_rows_without_spread_and_without_numbers():
     assert y[0].isnan().all()  # 0 * 1 / 0, as the formula says
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [7, 13, 1001, 1600])
+def test_an_infinite_gradient_at_a_row_s_end(cols, dt):
+    """dy infinite in the last column, in a slot that is moved back and so loads values that another one has: with
+    xhat = 1 in the row its two means are infinite, as the formula has them, and not NaN; no other row notices."""
+    x, dy, w = make(3, cols, dt, 1), make(3, cols, dt, 2), torch.ones(cols, dtype=DTS[dt], device=DEV)
+    mean, rstd = torch.zeros(3, device=DEV), torch.ones(3, device=DEV)
+    x[1] = 1.0
+    dy[1] = 1.0
+    dy[1, cols - 1] = float("inf")
+    dx, dw, db = torch.empty_like(x), torch.empty(cols, device=DEV), torch.empty(cols, device=DEV)
+    zdp.layer_norm_backward(dy, x, w, mean, rstd, dx, dw, db, workspace=zdp.new_workspace(1))
+    # mean(v) = mean(v xhat) = inf: 1 - inf - inf, and in the last column inf - inf
+    assert (dx[1, :cols - 1] == -float("inf")).all() and dx[1, cols - 1].isnan()
+    assert dx[0].isfinite().all() and dx[2].isfinite().all()
+    assert dw[:cols - 1].isfinite().all() and db[cols - 1] == float("inf")
+
+
 def test_norm_of_no_rows():
     w = torch.ones(16, device=DEV)
     x, ws = torch.empty(0, 16, device=DEV), zdp.new_workspace(1)

@@ -229,13 +229,7 @@ __global__ void __launch_bounds__(64 * W * G, 2) norm_grad_kernel(const NormGrad
   fetch(row);
   float weight[V][kVals], dw[V][kVals] = {}, db[V][kVals] = {};
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    // values that another slot has too get no weight: they add nothing to a
-    // row's sums, and the column sums are not taken from them
-    load_weight<DT>(N.weight, N.w_dt, slot(j).at, weight[j]);
-#pragma unroll
-    for (int e = 0; e < kVals; ++e) weight[j][e] = e >= slot(j).skip ? weight[j][e] : 0.f;
-  }
+  for (int j = 0; j < V; ++j) load_weight<DT>(N.weight, N.w_dt, slot(j).at, weight[j]);
   int turn = 0;
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * G; base < N.rows; base += step, row += step, turn ^= 1) {
     const bool mine = row < N.rows;
@@ -263,8 +257,11 @@ __global__ void __launch_bounds__(64 * W * G, 2) norm_grad_kernel(const NormGrad
       values(j, d, xhat, v);
 #pragma unroll
       for (int e = 0; e < kVals; ++e) {
-        s1 += v[e];
-        s2 = __builtin_fmaf(v[e], xhat[e], s2);
+        // values that another slot has too add nothing to the row's sums; of
+        // the column sums theirs are not taken
+        const bool own = e >= slot(j).skip;
+        s1 += own ? v[e] : 0.f;
+        s2 = __builtin_fmaf(own ? v[e] : 0.f, own ? xhat[e] : 0.f, s2);
         dw[j][e] = __builtin_fmaf(d[e], xhat[e], dw[j][e]);
         db[j][e] += d[e];
       }
