@@ -531,7 +531,8 @@ int zero_gated_product_backward(const void* dh, int64_t dh_ld, const void* x, in
 
 /* ---- testing --------------------------------------------------------------
  * Not an operation of the pages. Caps the blocks of every streaming launch
- * (update, second pass, averaging, scan, restore, cast) at max_blocks > 0, on
+ * (update, second pass, averaging, scan, restore, cast, and a layer's operators
+ * but for the products' tiles) at max_blocks > 0, on
  * top of each launch's own cap (2^21 tiles per launch; 65,536 blocks for the
  * second pass and the scan; 1,024 for the restore). Every streaming kernel
  * loops over the tiles its grid does not cover, so a small shard under a low

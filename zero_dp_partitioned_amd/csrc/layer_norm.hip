@@ -84,7 +84,10 @@ struct Slot {
 };
 
 // W waves a row, V 16-byte slots a lane; a block of one wave a row has four
-// rows. At least Vec<DT>::kVals columns.
+// rows. At least Vec<DT>::kVals columns. Measured: 16384 x 4096 bf16 50 us (5.4
+// TB/s), 8192 x 1600 fp16 12.7 (4.1), one row of 4096 3.0 in a graph. The output
+// goes past the caches, the input does not: with the hint on both the first took
+// 50.6 us and the second 13.9 instead of 13.3.
 template <int DT, int V, int W>
 __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) norm_kernel(const NormArgs N) {
   constexpr int kVals = Vec<DT>::kVals, kElem = Vec<DT>::kElem, kRows = W == 1 ? 4 : 1;
@@ -140,6 +143,8 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) norm_kernel(const NormA
 }
 
 // Rows too long for the registers of a block, or shorter than a slot: read three times.
+// 8192 x 16384 bf16 in registers takes 111 us; a row that is read again costs as
+// much more as the caches do not hold.
 constexpr int kLongThreads = 1024;
 
 template <int DT>
@@ -197,6 +202,9 @@ __host__ __device__ inline int64_t sums_pitch(int64_t cols) { return (cols + 3) 
 // end the block's groups add theirs in group order through LDS and the block
 // leaves one row of sums. The next row's loads are in flight while a row is
 // worked on. A block's groups take equally many turns, so that its barriers meet.
+// Measured, 16384 x 4096 bf16 with dresidual: 93-99 us (5.5-5.8 TB/s) and 4.7 for
+// the join; two blocks a CU instead of one are no faster there and 33 us instead of
+// 30 at 8192 x 1600. All of it goes past the caches (115 -> 107 us).
 template <int DT, int V, int W, int G, bool RES>
 __global__ void __launch_bounds__(64 * W * G, 2) norm_grad_kernel(const NormGradArgs N) {
   constexpr int kVals = Vec<DT>::kVals, kElem = Vec<DT>::kElem;
@@ -435,6 +443,8 @@ hipError_t norm_start(const NormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// As many waves a row as leave a lane two to four slots (us at 16384 x 4096 bf16:
+// four waves with two slots 49.7, two with four 54.4, eight with one 55.5).
 template <int DT>
 hipError_t norm_launch(const NormArgs& a, hipStream_t s) {
   const int64_t slots = ceil_div(a.cols, Vec<DT>::kVals);
