@@ -335,13 +335,23 @@ __global__ void __launch_bounds__(64 * W * G, 2) norm_grad_kernel(const NormGrad
     const int64_t pitch = sums_pitch(N.cols);
     float* const to = N.partials + blockIdx.x * 2 * pitch;
 #pragma unroll
-    for (int j = 0; j < V; ++j)
+    for (int j = 0; j < V; ++j) {
+      float* const at = to + slot(j).at;
+      if (slot(j).skip == 0) {
 #pragma unroll
-      for (int e = 0; e < kVals; ++e)
-        if (e >= slot(j).skip) {
-          to[slot(j).at + e] = dw[j][e];
-          to[pitch + slot(j).at + e] = db[j][e];
+        for (int q = 0; q < kVals; q += 4) {
+          *reinterpret_cast<f4*>(at + q) = (f4){dw[j][q], dw[j][q + 1], dw[j][q + 2], dw[j][q + 3]};
+          *reinterpret_cast<f4*>(at + pitch + q) = (f4){db[j][q], db[j][q + 1], db[j][q + 2], db[j][q + 3]};
         }
+      } else {
+#pragma unroll
+        for (int e = 0; e < kVals; ++e)
+          if (e >= slot(j).skip) {
+            at[e] = dw[j][e];
+            at[pitch + e] = db[j][e];
+          }
+      }
+    }
   }
 }
 
