@@ -453,8 +453,9 @@ int zero_mx_product(const void* a_codes, const void* a_scales, int64_t lda, cons
  * vector that the step writes, and their gradients go into the gradient copy that
  * it reads. Not an operation of the pages. Tensors are rows of `cols` values, `ld`
  * from row to row, aligned to their elements (16 bytes are not needed). Sums and
- * statistics are fp32, in an order that depends on the sizes only, and every
- * output is rounded once, to nearest even. A workspace is one of
+ * statistics are fp32, in an order that depends only on the sizes, types and
+ * alignment of a call and on which outputs it asks for, so results repeat bit for
+ * bit, and every output is rounded once, to nearest even. A workspace is one of
  * zero_workspace_bytes(); a call uses what the step's calls use only within one
  * call, so it may run between them. Outputs must not overlap inputs or each
  * other, but where a call says so. */

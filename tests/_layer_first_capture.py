@@ -13,7 +13,7 @@ import zero_dp_partitioned_amd as zdp  # noqa: E402
 
 # m, d, f: single tokens; the small tile with one and two stages in flight, masked and split; the middle and the large tile
 SIZES = [(1, 200, 300), (3, 200, 300), (33, 40, 300), (33, 520, 33), (70, 2048, 4096), (600, 640, 520), (2000, 1500, 200),
-         (1300, 2600, 2600), (1301, 2603, 2601), (4000, 2560, 72)]
+         (1300, 2600, 2600), (1301, 2603, 2601), (4000, 2560, 72), (1500, 1600, 640)]
 
 
 def main():

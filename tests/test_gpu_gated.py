@@ -134,6 +134,33 @@ def test_backward_of_whole_numbers(size, dt, ws):
     dwg.check()
 
 
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("size", [(1500, 1600, 640), (1501, 1600, 648), (1500, 1608, 1000), (500, 1600, 6400)], ids=str)
+def test_both_products_of_the_backward_pass_in_one_launch(size, dt, ws):
+    """Sizes whose dx and dw share a launch, against the two asked for one by one, with and without adding: exact."""
+    m, d, f = size
+    g, dtype = torch.Generator(device=DEV).manual_seed(m), DTS[dt]
+    x, wg, wu = (whole_numbers(g, r, d, dtype, 0.5) for r in (m, f, f))
+    gate, up = (whole_numbers(g, m, f, dtype, 0.9) * 2 for _ in range(2))
+    dh = whole_numbers(g, m, f, dtype, math.sqrt(100 / max(m, f)))
+    out = torch.float32 if m % 2 else dtype
+    dg, du = torch.empty_like(gate), torch.empty_like(up)
+    base = torch.randint(-8, 9, (f, d), generator=g, device=DEV).to(out)
+    dx, a, b = Blank(m, d, dtype, 8), Blank(f, d, out, 8), Blank(f, d, out, 8)
+    for accumulate in (False, True):
+        for t in (a.t, b.t):
+            t.copy_(base)
+        zdp.gated_product_backward(dh, x, wg, wu, gate, up, dg, du, ws, dx=dx.t, dw_gate=a.t, dw_up=b.t, act="relu",
+                                   accumulate=accumulate)
+        G, H = dg.double(), du.double()
+        extra = base.double() if accumulate else 0
+        same(dx.t, G @ wg.double() + H @ wu.double(), "dx")
+        same(a.t, G.t() @ x.double() + extra, "dw_gate")
+        same(b.t, H.t() @ x.double() + extra, "dw_up")
+        for o in (dx, a, b):
+            o.check()
+
+
 # --------------------------------------------------------------------------
 # random values
 # --------------------------------------------------------------------------

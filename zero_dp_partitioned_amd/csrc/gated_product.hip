@@ -251,20 +251,19 @@ __device__ __forceinline__ uint32_t tiles_of(int64_t n, uint32_t size) { return 
 // wave a SIMD shows every wait. Higher priority for one wave of each SIMD, or around
 // the products, changed 1 % either way.
 template <Use USE, Fetch FETCH, int FM, int FN, int WM, int WN, int NB, int KG, int DT, int ODT>
-__global__ void __launch_bounds__(64 * WM * WN * KG, 2) gated_tile_kernel(const ProductArgs P) {
+__device__ __forceinline__ void gated_tile(const ProductArgs& P, uint32_t block, uint8_t* lds) {
   using T = Tile<USE, FM, FN, WM, WN, NB, KG>;
   using A = typename T::A;
   using B = typename T::B;
-  extern __shared__ __align__(1024) uint8_t lds[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = KG > 1 ? wave / T::kWaves : 0, w = KG > 1 ? wave % T::kWaves : wave;
   const uint32_t tiles_m = tiles_of(P.m, T::kM), tiles_n = tiles_of(P.n, T::kOutN);
   const uint32_t rows = USE == kDw ? 2 * tiles_m : tiles_m;  // dwu's tiles behind dwg's
-  const uint32_t split = P.splits > 1 ? blockIdx.x / (rows * tiles_n) : 0;
+  const uint32_t split = P.splits > 1 ? block / (rows * tiles_n) : 0;
   uint32_t tm, tn;
   // (4 or 8 tile rows a group, us at 8192 x 4096 x 14336: forward 1457 or 1414, dx 1416 or 1365, dw 1379 or 1439)
-  tile_of<USE == kDw ? 4 : 8>(P.splits > 1 ? blockIdx.x % (rows * tiles_n) : blockIdx.x, rows, tiles_n, &tm, &tn);
+  tile_of<USE == kDw ? 4 : 8>(P.splits > 1 ? block % (rows * tiles_n) : block, rows, tiles_n, &tm, &tn);
   const int z = USE == kDw && tm >= tiles_m;  // which output
   if (z) tm -= tiles_m;
   // The tile's first row and column, and the first of the operands': along the
@@ -608,6 +607,24 @@ __global__ void __launch_bounds__(64 * WM * WN * KG, 2) gated_tile_kernel(const 
   }
 }
 
+template <Use USE, Fetch FETCH, int FM, int FN, int WM, int WN, int NB, int KG, int DT, int ODT>
+__global__ void __launch_bounds__(64 * WM * WN * KG, 2) gated_tile_kernel(const ProductArgs P) {
+  extern __shared__ __align__(1024) uint8_t lds[];
+  gated_tile<USE, FETCH, FM, FN, WM, WN, NB, KG, DT, ODT>(P, blockIdx.x, lds);
+}
+
+// dx and dw in one launch, for sizes whose blocks fill neither's last round over
+// the CUs: `first` blocks of dx's middle tiles (those behind `of_dx` have nothing to
+// do, so that dw's blocks stand on the XCDs that their mapping expects), then dw's
+// large ones. Either takes a CU's LDS.
+template <int DT, int ODT>
+__global__ void __launch_bounds__(512, 2) gated_pair_kernel(const ProductArgs X, const ProductArgs W, uint32_t of_dx,
+                                                            uint32_t first) {
+  extern __shared__ __align__(1024) uint8_t lds[];
+  if (blockIdx.x >= first) gated_tile<kDw, kDirect, 8, 4, 2, 4, 2, 1, DT, ODT>(W, blockIdx.x - first, lds);
+  else if (blockIdx.x < of_dx) gated_tile<kDx, kDirect, 2, 4, 4, 2, 4, 1, DT, DT>(X, blockIdx.x, lds);
+}
+
 // ------------------------------------------------------------------------
 // Forward for very few rows, kTokens of them at most, which is one pass over the
 // weights: a block takes 16 rows of wg and the same of wu. A wave takes runs of
@@ -786,6 +803,21 @@ __global__ void __launch_bounds__(256) gate_grad_kernel(const GateGradArgs G, in
 // Launches
 // ------------------------------------------------------------------------
 
+// More than the default limit of 64 KiB of dynamic LDS, granted once per kernel and device.
+template <typename Kernel>
+hipError_t grant_lds(Kernel kernel, int lds, std::atomic<uint64_t>& granted) {
+  int dev = 0;
+  if (hipError_t e = hipGetDevice(&dev)) return e;
+  const uint64_t bit = uint64_t{1} << (dev & 63);
+  if (dev > 63 || !(granted.load(std::memory_order_acquire) & bit)) {
+    if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, lds))
+      return e;
+    granted.fetch_or(bit, std::memory_order_release);
+  }
+  return hipSuccess;
+}
+
 template <Use USE, Fetch FETCH, int FM, int FN, int WM, int WN, int NB, int KG, int DT, int ODT>
 hipError_t tile_launch(const ProductArgs& a, hipStream_t s) {
   using T = Tile<USE, FM, FN, WM, WN, NB, KG>;
@@ -793,17 +825,8 @@ hipError_t tile_launch(const ProductArgs& a, hipStream_t s) {
   const int64_t tiles = ceil_div(a.m, T::kM) * ceil_div(a.n, T::kOutN) * (USE == kDw ? 2 : 1);
   if (tiles > INT32_MAX / T::kThreads / (a.splits > 1 ? a.splits : 1)) return hipErrorInvalidConfiguration;
   if (a.dry) return hipSuccess;
-  // more than the default limit of 64 KiB of dynamic LDS, granted once per kernel and device
   static std::atomic<uint64_t> granted{0};
-  int dev = 0;
-  if (hipError_t e = hipGetDevice(&dev)) return e;
-  const uint64_t bit = uint64_t{1} << (dev & 63);
-  if (dev > 63 || !(granted.load(std::memory_order_acquire) & bit)) {
-    if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds))
-      return e;
-    granted.fetch_or(bit, std::memory_order_release);
-  }
+  if (hipError_t e = grant_lds(kernel, T::kLds, granted)) return e;
   const int64_t blocks = tiles * (a.splits > 1 ? a.splits : 1);
   hipLaunchKernelGGL(kernel, dim3(static_cast<uint32_t>(blocks)), dim3(T::kThreads), T::kLds, s, a);
   return hipGetLastError();
@@ -817,6 +840,14 @@ constexpr int64_t kMostCus = 208;
 constexpr int64_t kFewSmall = 448;
 constexpr int64_t kVeryFew = 128;
 
+// Whether every slot of the operands is aligned and whole. (A moved tile starts at
+// n - kN: on 16 bytes if n is.)
+template <Use USE>
+bool direct_fetch(const ProductArgs& a) {
+  return aligned16(a.a[0], a.a_ld) && aligned16(a.b[0], a.b_ld) && (!a.a[1] || aligned16(a.a[1], a.a_ld)) &&
+         (!a.b[1] || aligned16(a.b[1], a.b_ld)) && (USE != kDw || a.m % 8 == 0) && (USE == kForward || a.n % 8 == 0);
+}
+
 // One tile shape with the fetch that the operands allow; fetches that write LDS
 // themselves keep NB - 1 stages in flight.
 template <Use USE, int FM, int FN, int WM, int WN, int NB, int KG, int DT, int ODT>
@@ -825,13 +856,16 @@ hipError_t fetch_launch(const ProductArgs& a, hipStream_t s) {
   if constexpr (T::kM == 64 && USE != kForward) {
     if ((USE == kDw && a.m < T::kM) || a.n < T::kN) return tile_launch<USE, kMasked, FM, FN, WM, WN, 2, KG, DT, ODT>(a, s);
   }
-  // a moved tile starts at n - kN: on 16 bytes if n is
-  bool direct = aligned16(a.a[0], a.a_ld) && aligned16(a.b[0], a.b_ld) && (!a.a[1] || aligned16(a.a[1], a.a_ld)) &&
-                (!a.b[1] || aligned16(a.b[1], a.b_ld));
-  if (USE == kDw) direct = direct && a.m % 8 == 0;
-  if (USE != kForward) direct = direct && a.n % 8 == 0;
-  if (direct) return tile_launch<USE, kDirect, FM, FN, WM, WN, NB, KG, DT, ODT>(a, s);
+  if (direct_fetch<USE>(a)) return tile_launch<USE, kDirect, FM, FN, WM, WN, NB, KG, DT, ODT>(a, s);
   return tile_launch<USE, kStaged, FM, FN, WM, WN, 2, KG, DT, ODT>(a, s);
+}
+
+template <int ODT>
+hipError_t join_launch(const ProductArgs& a, int outputs, hipStream_t s) {
+  const int64_t blocks = ceil_div(a.m * a.n, 256);
+  hipLaunchKernelGGL((gated_join_kernel<ODT>), dim3(static_cast<uint32_t>(blocks < 4096 ? blocks : 4096), outputs), dim3(256),
+                     0, s, a, outputs);
+  return hipGetLastError();
 }
 
 template <Use USE, int DT, int ODT>
@@ -904,10 +938,47 @@ hipError_t product_launch(ProductArgs a, float* scratch, hipStream_t s) {
   else if (blocks <= kFewSmall) e = fetch_launch<USE, 2, 4, 2, 2, 3, 1, DT, ODT>(a, s);
   else e = fetch_launch<USE, 2, 4, 2, 2, 2, 1, DT, ODT>(a, s);
   if (e != hipSuccess || a.splits <= 1 || a.dry) return e;
-  const int64_t join = ceil_div(a.m * a.n, 256);
-  hipLaunchKernelGGL((gated_join_kernel<ODT>), dim3(static_cast<uint32_t>(join < 4096 ? join : 4096), kOutputs), dim3(256),
-                     0, s, a, kOutputs);
-  return hipGetLastError();
+  return join_launch<ODT>(a, kOutputs, s);
+}
+
+// dx and dw together, if that pays: *done says whether they were launched. By an
+// estimate in which a stage of a middle tile takes 0.55 us, one of a large tile 1.45
+// and its ends 6, and the last blocks run half a large tile past the rest (the whole
+// backward pass, us apart and together, and the estimate's ratio: 1500 x 1600 x 6400
+// 211, 171, 0.75; 2048 rows 237, 224, 0.87; 500 rows 94, 88, 0.88; 1001 rows 142, 139.5,
+// 0.88; 600 x 800 x 3200 42, 47, 0.92; 1000 x 1024 x 4096 64, 70, 1.0).
+template <int DT, int ODT>
+hipError_t pair_launch(ProductArgs x, ProductArgs w, float* scratch, hipStream_t s, bool* done) {
+  using X = Tile<kDx, 2, 4, 4, 2, 4>;
+  using W = Tile<kDw, 8, 4, 2, 4, 2>;
+  *done = false;
+  if (x.m <= X::kM / 2 || x.n < X::kN || w.m < W::kM || w.n < W::kN || !direct_fetch<kDx>(x) || !direct_fetch<kDw>(w))
+    return hipSuccess;
+  const int64_t tiles_x = ceil_div(x.m, X::kM) * ceil_div(x.n, X::kN), tiles_w = 2 * ceil_div(w.m, W::kM) * ceil_div(w.n, W::kN);
+  if (tiles_x > kCus || tiles_w > 4 * kCus) return hipSuccess;
+  const int64_t chunks = 2 * ceil_div(x.k, kChunk);
+  const int64_t room = static_cast<int64_t>(kScratchBytes / sizeof(float)) / (x.m * x.n);
+  int64_t splits = kCus / tiles_x;
+  splits = splits < room ? splits : room;
+  splits = splits < chunks / 4 ? splits : chunks / 4;
+  splits = splits > 1 ? splits : 1;
+  const double tx = 0.55 * chunks / splits, tw = 1.45 * ceil_div(w.k, kChunk) + 6;
+  const double apart = tx + tw * ceil_div(tiles_w, kCus), together = (tx * tiles_x * splits + tw * tiles_w) / kCus;
+  if (together + 0.5 * tw > 0.9 * apart) return hipSuccess;
+  *done = true;
+  x.splits = static_cast<int32_t>(splits);
+  x.partial = scratch;
+  w.splits = 1;
+  w.partial = nullptr;
+  const auto kernel = gated_pair_kernel<DT, ODT>;
+  constexpr int kLds = X::kLds > W::kLds ? X::kLds : W::kLds;
+  static_assert(X::kThreads == 512 && W::kThreads == 512, "");
+  static std::atomic<uint64_t> granted{0};
+  if (hipError_t e = grant_lds(kernel, kLds, granted)) return e;
+  const uint32_t of_dx = static_cast<uint32_t>(tiles_x * splits), first = (of_dx + kXcds - 1) / kXcds * kXcds;
+  hipLaunchKernelGGL(kernel, dim3(first + static_cast<uint32_t>(tiles_w)), dim3(512), kLds, s, x, w, of_dx, first);
+  if (hipError_t e = hipGetLastError()) return e;
+  return splits > 1 ? join_launch<DT>(x, 1, s) : hipSuccess;
 }
 
 template <int DT>
@@ -928,49 +999,45 @@ hipError_t forward_launch(const GatedArgs& g, hipStream_t s) {
   return product_launch<kForward, DT, DT>(a, nullptr, s);
 }
 
-template <int DT>
+template <int DT, int ODT>
 hipError_t products_of_grad(const GatedGradArgs& g, bool dry, hipStream_t s) {
-  ProductArgs a = {};
-  a.dry = dry;
-  if (g.dx.p && g.m > 0 && g.d > 0) {
-    for (int i = 0; i < 2; ++i) {
-      a.a[i] = static_cast<const char*>(g.dpre[i].p);
-      a.b[i] = static_cast<const char*>(g.w[i].p);
-    }
-    a.a_ld = g.dpre[0].ld * 2;
-    a.b_ld = g.w[0].ld * 2;
-    a.m = g.m;
-    a.n = g.d;
-    a.k = g.f;
-    a.out[0] = g.dx.p;
-    a.out_ld[0] = g.dx.ld;
-    if (hipError_t e = product_launch<kDx, DT, DT>(a, g.scratch, s)) return e;
+  ProductArgs x = {}, w = {};
+  x.dry = w.dry = dry;
+  for (int i = 0; i < 2; ++i) {
+    x.a[i] = w.a[i] = static_cast<const char*>(g.dpre[i].p);
+    x.b[i] = static_cast<const char*>(g.w[i].p);
+    w.out[i] = g.dw[i].p;
+    w.out_ld[i] = g.dw[i].ld;
   }
-  if (g.dw[0].p && g.f > 0 && g.d > 0) {
-    a = {};
-    a.dry = dry;
-    for (int i = 0; i < 2; ++i) {
-      a.a[i] = static_cast<const char*>(g.dpre[i].p);
-      a.out[i] = g.dw[i].p;
-      a.out_ld[i] = g.dw[i].ld;
-    }
-    a.b[0] = static_cast<const char*>(g.x.p);
-    a.a_ld = g.dpre[0].ld * 2;
-    a.b_ld = g.x.ld * 2;
-    a.m = g.f;
-    a.n = g.d;
-    a.k = g.m;
-    a.accumulate = g.accumulate;
-    if (g.dw_dt == ZERO_DT_F32) return product_launch<kDw, DT, ZERO_DT_F32>(a, g.scratch, s);
-    return product_launch<kDw, DT, DT>(a, g.scratch, s);
+  x.a_ld = w.a_ld = g.dpre[0].ld * 2;
+  x.b_ld = g.w[0].ld * 2;
+  x.m = g.m;
+  x.n = g.d;
+  x.k = g.f;
+  x.out[0] = g.dx.p;
+  x.out_ld[0] = g.dx.ld;
+  w.b[0] = static_cast<const char*>(g.x.p);
+  w.b_ld = g.x.ld * 2;
+  w.m = g.f;
+  w.n = g.d;
+  w.k = g.m;
+  w.accumulate = g.accumulate;
+  const bool of_x = g.dx.p && g.m > 0 && g.d > 0, of_w = g.dw[0].p && g.f > 0 && g.d > 0;
+  if (of_x && of_w && !dry) {
+    bool done = false;
+    const hipError_t e = pair_launch<DT, ODT>(x, w, g.scratch, s, &done);
+    if (done || e != hipSuccess) return e;
   }
-  return hipSuccess;
+  if (of_x)
+    if (hipError_t e = product_launch<kDx, DT, DT>(x, g.scratch, s)) return e;
+  return of_w ? product_launch<kDw, DT, ODT>(w, g.scratch, s) : hipSuccess;
 }
 
 template <int DT>
 hipError_t grad_launch(const GatedGradArgs& g, hipStream_t s) {
   // a call that cannot launch all of it launches nothing
-  if (hipError_t e = products_of_grad<DT>(g, true, s)) return e;
+  const bool wide = g.dw_dt == ZERO_DT_F32;
+  if (hipError_t e = wide ? products_of_grad<DT, ZERO_DT_F32>(g, true, s) : products_of_grad<DT, DT>(g, true, s)) return e;
   if (g.m > 0 && g.f > 0) {
     GateGradArgs e = {g.dh, {g.pre[0], g.pre[1]}, {g.dpre[0], g.dpre[1]}, g.m, g.f, g.act};
     if (g.dh.ld == g.f && g.pre[0].ld == g.f && g.dpre[0].ld == g.f) {  // one row
@@ -982,7 +1049,7 @@ hipError_t grad_launch(const GatedGradArgs& g, hipStream_t s) {
     hipLaunchKernelGGL((gate_grad_kernel<DT>), dim3(grid), dim3(256), 0, s, e, row_slots, slots);
     if (hipError_t x = hipGetLastError()) return x;
   }
-  return products_of_grad<DT>(g, false, s);
+  return wide ? products_of_grad<DT, ZERO_DT_F32>(g, false, s) : products_of_grad<DT, DT>(g, false, s);
 }
 
 }  // namespace

@@ -202,7 +202,7 @@ __host__ __device__ inline int64_t sums_pitch(int64_t cols) { return (cols + 3) 
 // end the block's groups add theirs in group order through LDS and the block
 // leaves one row of sums. The next row's loads are in flight while a row is
 // worked on. A block's groups take equally many turns, so that its barriers meet.
-// Measured, 16384 x 4096 bf16 with dresidual: 93-99 us (5.5-5.8 TB/s) and 4.7 for
+// Measured, 16384 x 4096 bf16 with dresidual: 91-92 us (5.8-5.9 TB/s) and 4.6 for
 // the join; two blocks a CU instead of one are no faster there and 33 us instead of
 // 30 at 8192 x 1600. All of it goes past the caches (115 -> 107 us).
 template <int DT, int V, int W, int G, bool RES>
