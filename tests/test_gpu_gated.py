@@ -343,3 +343,30 @@ def test_results_repeat(ws):
         zdp.gated_product_backward(dh, x, w, w, gate, gate, dg, du, ws, dx=dx, dw_gate=a, dw_up=b)
         seen.append((h, dx, a, b))
     assert all(torch.equal(p, q) for s in seen[1:] for p, q in zip(seen[0], s))
+
+
+def gates(dtype):
+    """Finite gates over a type's whole range, both signs."""
+    top = torch.finfo(dtype).max
+    g = [0.0, 2.0 ** -14, 1.0, 13.3, 30.0, 63.0, 64.0, 65.0, 100.0, 1e4, top] + [1e10, 4e19, 6e19, 1e20, 1e30] * (top > 1e38)
+    return torch.tensor([s * v for v in g for s in (1, -1)], dtype=torch.float64).to(dtype)
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("act", ACTS)
+def test_gradients_at_gates_of_any_size(act, dt, ws):
+    """Finite gates give the formulas' finite gradients, however large (with dh = up = 1 dgate is the derivative itself
+    and dup the activation). The errors up to |z| = 16 are those of test_backward; past it the smaller of sigmoid(z) and
+    sigmoid(-z) is under 2^-23, so that what it is off by is lost beside the few u of the products."""
+    dtype = DTS[dt]
+    gate = gates(dtype).to(DEV).view(2, -1)
+    m, f = gate.shape
+    one, x, w = torch.ones_like(gate), torch.zeros(m, 8, dtype=dtype, device=DEV), torch.zeros(f, 8, dtype=dtype, device=DEV)
+    dg, du = torch.empty_like(gate), torch.empty_like(gate)
+    zdp.gated_product_backward(one, x, w, w, gate, one, dg, du, ws, act=act)
+    Z = gate.double().cpu()
+    A, _ = act_of(Z, act)
+    DA = act_of(Z.clamp(-100, 100), act)[1]  # past that it has reached its limit, to e^-95
+    low, eda = Z.abs() <= 16, act_error(Z, 1 + Z.abs() / 2)
+    close(dg.cpu(), DA, torch.where(low, eda, 8 * U), "dgate")
+    close(du.cpu(), A, torch.where(low, act_error(Z, A), 8 * U * (A.abs() + 1)) + 2 * U * A.abs(), "dup")

@@ -85,8 +85,11 @@ __device__ __forceinline__ void activation_grad(float g, int32_t act, float* a, 
     }
     case ZERO_ACT_GELU_TANH: {
       const float z = kTanhA * g * __builtin_fmaf(kTanhB * g, g, 1.f), s = sigmoid(z), r = sigmoid(-z);
+      // past 64 one of s and r is 0, and so is the term with the slope of z, which
+      // g's own square would make 0 times infinity from 5e19 on
+      const float c = __builtin_fminf(__builtin_fmaxf(g, -64.f), 64.f);
       *a = g * s;
-      *da = __builtin_fmaf(*a * r, kTanhA * __builtin_fmaf(3.f * kTanhB * g, g, 1.f), s);
+      *da = __builtin_fmaf(*a * r, kTanhA * __builtin_fmaf(3.f * kTanhB * c, c, 1.f), s);
       return;
     }
     case ZERO_ACT_RELU:
