@@ -370,3 +370,45 @@ def test_gradients_at_gates_of_any_size(act, dt, ws):
     low, eda = Z.abs() <= 16, act_error(Z, 1 + Z.abs() / 2)
     close(dg.cpu(), DA, torch.where(low, eda, 8 * U), "dgate")
     close(du.cpu(), A, torch.where(low, act_error(Z, A), 8 * U * (A.abs() + 1)) + 2 * U * A.abs(), "dup")
+
+
+@pytest.mark.parametrize("act, lo, hi", [("silu", 60, 104), ("sigmoid", 60, 104), ("gelu", 10, 14), ("gelu_tanh", 8, 11)])
+def test_small_values_of_far_gates(act, lo, hi, ws):
+    """bf16 reaches down to 2^-133, and so do the activations and their derivatives at far gates. What they are off by,
+    relative to the activation: its argument is rounded, |argument| u of the exponential at each rounding of it (silu one,
+    gelu_tanh four; gelu's erfc, whose own error is 16 units at most, moves by z^2 of its argument's), and a few u more;
+    and what falls below fp32's normal values is rounded at 2^-149."""
+    g = torch.linspace(lo, hi, 353, dtype=torch.float64).bfloat16().unique()
+    gate = torch.stack([-g, g]).to(DEV)
+    m, f = gate.shape
+    one, x, w = (torch.ones_like(gate), torch.zeros(m, 8, dtype=gate.dtype, device=DEV),
+                 torch.zeros(f, 8, dtype=gate.dtype, device=DEV))
+    dg, du = torch.empty_like(gate), torch.empty_like(gate)
+    zdp.gated_product_backward(one, x, w, w, gate, one, dg, du, ws, act=act)
+    Z = gate.double()
+    z = Z.abs()
+    A, DA = act_of(Z, act)
+    rel = {"silu": 2 * z, "sigmoid": 2 * z, "gelu": 2 * z * z + 32, "gelu_tanh": 4 * (1.6 * z + 0.0714 * z ** 3)}[act] * U + 16 * U
+    tail, step = act_of(-z, act)[0].abs(), 2.0 ** -149
+    slope = 2 + 0.3 * z * z  # at least that of the argument, and |z|, by which gelu's density exceeds the tail
+    ea = rel * tail + 8 * U * A.abs() + step * (1 + z)
+    close(du, A, ea, "dup")
+    close(dg, DA, rel * tail * slope + 8 * U * DA.abs() + step * (2 + (1 + z) * slope), "dgate")
+    assert (tail > 2.0 ** -126).any() and (tail < 2.0 ** -126).any()
+    # the forward pass: products of one term, by the kernel of single tokens and by tiles, among gates that are not far
+    # and get the same bits without far ones beside them
+    near = torch.linspace(-3, 3, f, device=DEV).bfloat16()
+    for rows in (1, 5, 300):
+        x1, wu = (torch.zeros(r, 8, dtype=gate.dtype, device=DEV) for r in (rows, f))
+        x1[:, 0], wu[:, 0] = 1, 1
+
+        def forward(gates):
+            w = torch.zeros(f, 8, dtype=gate.dtype, device=DEV)
+            w[:, 0] = gates
+            h = torch.empty(rows, f, dtype=gate.dtype, device=DEV)
+            zdp.gated_product(x1, w, wu, h, act)
+            return h
+        close(forward(gate[0]), A[:1].expand(rows, f), ea[:1], f"h of {rows} rows")
+        odd = torch.arange(f, device=DEV) % 2 == 1
+        mixed, alone = forward(torch.where(odd, gate[0], near)), forward(near)
+        assert torch.equal(mixed[:, ~odd], alone[:, ~odd])
