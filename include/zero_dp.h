@@ -463,6 +463,9 @@ int zero_mx_product(const void* a_codes, const void* a_scales, int64_t lda, cons
 /* Layer norm over each row of x (F32, F16 or BF16): with mean and var (the mean
  * square of x - mean) of the row and rstd = 1 / sqrt(var + eps),
  *   y = (x - mean) * rstd * weight + bias.
+ * A row's sums may pass fp32's range (its squares do from a spread of 1e19 on); a
+ * row is NaN if it holds an infinity or NaN, or a value farther from the mean than
+ * fp32 reaches. Rows of no values leave y, mean and rstd as they are.
  * weight and bias have `cols` values of w_dt: x's type or F32; bias may be NULL.
  * mean and rstd (fp32, one a row, what the backward pass reads) are written unless
  * both are NULL.

@@ -202,6 +202,53 @@ def test_an_infinite_gradient_at_a_row_s_end(cols, dt):
     assert dw[:cols - 1].isfinite().all() and db[cols - 1] == float("inf")
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [3, 5, 64, 1000, 1600, 4096, 9000, 33000])
+def test_norm_of_rows_whose_sums_pass_fp32(cols, dt):
+    """Rows whose squares, or whose values' sums, pass fp32's range have their statistics like any others. The bounds are
+    test_norm's: the sums are then those of values times a power of two."""
+    g = np.random.default_rng(cols)
+    n = g.normal(size=(8, cols))
+    x = np.stack([n[0], n[1] * 1e20, n[2] * 1e30, np.abs(n[3]) * 3e37, 1e38 * (1 + 0.01 * n[4].clip(-5, 5)),
+                  1.2e38 * np.sign(n[5]), n[6] * 1e25 + 1e27, n[7]])
+    x = wide(x, dt)
+    w, b = (make(1, cols, "f32", cols + k)[0] for k in (1, 2))
+    y, mean, rstd = torch.empty_like(x), torch.empty(8, device=DEV), torch.empty(8, device=DEV)
+    zdp.layer_norm(x, w, b, y, 1e-5, mean=mean, rstd=rstd)
+    X, W, B = f64(x), f64(w), f64(b)
+    Y, M, R = _layer.norm(X, W, B, 1e-5)
+    k = depth(cols) + 3
+    dmean = (k * U * np.abs(X).mean(1) + U * np.abs(M))[:, None]
+    close(mean, M, dmean[:, 0], "mean")
+    d = np.abs(X - M[:, None])
+    shift = np.sqrt(((dmean + U * d) ** 2).mean(1, keepdims=True)) * R[:, None]
+    drstd = R[:, None] * ((k / 2 + 4) * U + shift + shift ** 2)
+    close(rstd, R, drstd[:, 0], "rstd")
+    err = (dmean + 2 * U * d) * R[:, None] + d * drstd
+    close(y, Y, np.abs(W) * err + 4 * U * (np.abs(W) * d * R[:, None] + np.abs(B)), "y")
+    # the backward pass takes such statistics
+    dy, dx = make(8, cols, dt, cols + 5), torch.empty_like(x)
+    zdp.layer_norm_backward(dy, x, w, mean, rstd, dx)
+    M, R, D = f64(mean)[:, None], f64(rstd)[:, None], f64(dy)
+    DX = _layer.norm_grad(D, X, W, M[:, 0], R[:, 0])[0]
+    xhat, v = np.abs((X - M) * R), np.abs(D * W)
+    c1, c2 = v.mean(1, keepdims=True), (v * xhat).mean(1, keepdims=True)
+    err = R * ((k + 4) * U * c1 + (k + 8) * U * xhat * c2 + 6 * U * (v + c1 + xhat * c2))
+    close(dx, DX, err + 2 * U * np.abs(DX), "dx")
+
+
+@pytest.mark.parametrize("cols", [5, 100, 1600, 33000])
+def test_norm_rows_that_fp32_cannot_hold_are_nan(cols):
+    """Infinities, NaN, and distances from the mean past fp32's range; the rows beside them do not notice."""
+    x = torch.randn(9, cols, device=DEV)
+    x[1, 2], x[3, 2], x[5, 2] = float("inf"), float("nan"), -float("inf")
+    x[7] = -3e38
+    x[7, 0] = 3e38
+    w, y, mean, rstd = torch.ones(cols, device=DEV), torch.empty_like(x), torch.empty(9, device=DEV), torch.empty(9, device=DEV)
+    zdp.layer_norm(x, w, w, y, mean=mean, rstd=rstd)
+    assert y[1::2].isnan().all() and y[::2].isfinite().all() and rstd[1::2].isnan().all()
+
+
 def test_norm_of_no_rows():
     w = torch.ones(16, device=DEV)
     x, ws = torch.empty(0, 16, device=DEV), zdp.new_workspace(1)

@@ -44,6 +44,37 @@ __device__ __forceinline__ float row_sum(float x, float* part, int w, int lane) 
   return x;
 }
 
+// Rows whose sums pass fp32's range, though their values do not: the sums are
+// formed again from values times a power of two, and the results scaled back. (Sums of
+// both signs may have come to NaN.) Every wave of a row gets here or none does.
+// `again(scale)` gives this lane's share of the scaled sum. A row whose distances
+// from the mean pass the range too, or that holds an infinity or NaN, is NaN.
+constexpr float kMeanScale = 0x1p-20f;    // 2^20 values below 2^128
+constexpr float kSquareScale = 0x1p-76f;  // 2^20 squares of values below 2^128
+
+template <int W, typename Again>
+__device__ __forceinline__ float row_sum_scaled(float scale, float* part, int w, int lane, Again&& again) {
+  if constexpr (W > 1) __syncthreads();  // `part` has been read
+  const float s = row_sum<W>(again(scale), part, w, lane);
+  if constexpr (W > 1) __syncthreads();
+  return s;
+}
+
+template <int W, typename Again>
+__device__ __forceinline__ float row_mean(float sum, float inv, float* part, int w, int lane, Again&& again) {
+  sum = row_sum<W>(sum, part, w, lane);
+  if (__builtin_isfinite(sum)) return sum * inv;
+  return row_sum_scaled<W>(kMeanScale, part, w, lane, again) * inv * (1.f / kMeanScale);
+}
+
+template <int W, typename Again>
+__device__ __forceinline__ float row_rstd(float sq, float inv, float eps, float* part, int w, int lane, Again&& again) {
+  sq = row_sum<W>(sq, part, w, lane);
+  if (!__builtin_isinf(sq)) return 1.0f / sqrtf(sq * inv + eps);
+  sq = row_sum_scaled<W>(kSquareScale, part, w, lane, again);
+  return 1.0f / sqrtf(sq * inv + eps * kSquareScale * kSquareScale) * kSquareScale + (sq - sq);  // NaN for infinity
+}
+
 // Vec<DT>::kVals values of the weight (or bias), of x's type or fp32, from column `col` on.
 template <int DT>
 __device__ __forceinline__ void load_weight(const void* p, int32_t w_dt, int col, float* v) {
@@ -101,28 +132,37 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) norm_kernel(const NormA
     u4 raw[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) raw[j] = Slot<DT, W>(j, w, lane, N.cols).load(x);
-    float sum = 0.f;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const Slot<DT, W> slot(j, w, lane, N.cols);
-      widen<DT>(raw[j], v[j]);
+    for (int j = 0; j < V; ++j) widen<DT>(raw[j], v[j]);
+    auto share = [&](float scale) {
+      float sum = 0.f;
 #pragma unroll
-      for (int e = 0; e < kVals; ++e) sum += e >= slot.skip ? v[j][e] : 0.f;
-    }
-    const float mean = row_sum<W>(sum, part, w, lane) * inv;
-    float sq = 0.f;
+      for (int j = 0; j < V; ++j) {
+        const Slot<DT, W> slot(j, w, lane, N.cols);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const Slot<DT, W> slot(j, w, lane, N.cols);
-#pragma unroll
-      for (int e = 0; e < kVals; ++e) {
-        v[j][e] -= mean;
-        const float d = e >= slot.skip ? v[j][e] : 0.f;
-        sq = __builtin_fmaf(d, d, sq);
+        for (int e = 0; e < kVals; ++e) sum += e >= slot.skip ? v[j][e] * scale : 0.f;
       }
-    }
-    const float var = row_sum<W>(sq, part + W, w, lane) * inv;
-    const float rstd = 1.0f / sqrtf(var + N.eps);
+      return sum;
+    };
+    const float mean = row_mean<W>(share(1.f), inv, part, w, lane, share);
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int e = 0; e < kVals; ++e) v[j][e] -= mean;
+    auto squares = [&](float scale) {
+      float sq = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const Slot<DT, W> slot(j, w, lane, N.cols);
+#pragma unroll
+        for (int e = 0; e < kVals; ++e) {
+          const float d = e >= slot.skip ? v[j][e] * scale : 0.f;
+          sq = __builtin_fmaf(d, d, sq);
+        }
+      }
+      return sq;
+    };
+    const float rstd = row_rstd<W>(squares(1.f), inv, N.eps, part + W, w, lane, squares);
     if (N.mean && lane == 0 && w == 0) {
       N.mean[row] = mean;
       N.rstd[row] = rstd;
@@ -162,19 +202,25 @@ __global__ void __launch_bounds__(kLongThreads) norm_long_kernel(const NormArgs 
         f(col, v);
       }
     };
-    float sum = 0.f;
-    each([&](int, const float* v) {
-      for (int e = 0; e < kVals; ++e) sum += v[e];
-    });
-    const float mean = row_sum<kWaves>(sum, part, w, lane) * inv;
-    float sq = 0.f;
-    each([&](int col, const float* v) {
-      for (int e = 0; e < kVals; ++e) {
-        const float d = col + e < N.cols ? v[e] - mean : 0.f;
-        sq = __builtin_fmaf(d, d, sq);
-      }
-    });
-    const float rstd = 1.0f / sqrtf(row_sum<kWaves>(sq, part + kWaves, w, lane) * inv + N.eps);
+    auto share = [&](float scale) {
+      float sum = 0.f;
+      each([&](int, const float* v) {
+        for (int e = 0; e < kVals; ++e) sum += v[e] * scale;
+      });
+      return sum;
+    };
+    const float mean = row_mean<kWaves>(share(1.f), inv, part, w, lane, share);
+    auto squares = [&](float scale) {
+      float sq = 0.f;
+      each([&](int col, const float* v) {
+        for (int e = 0; e < kVals; ++e) {
+          const float d = col + e < N.cols ? (v[e] - mean) * scale : 0.f;
+          sq = __builtin_fmaf(d, d, sq);
+        }
+      });
+      return sq;
+    };
+    const float rstd = row_rstd<kWaves>(squares(1.f), inv, N.eps, part + kWaves, w, lane, squares);
     if (N.mean && threadIdx.x == 0) {
       N.mean[row] = mean;
       N.rstd[row] = rstd;
