@@ -78,7 +78,9 @@ int zero_layer_norm(const void* x, int32_t dt, int64_t rows, int64_t cols, int64
                     const void* bias, int32_t w_dt, double eps, void* y, int64_t y_ld, float* mean, float* rstd,
                     void* stream) {
   if (int rc = check_norm(dt, w_dt, rows, cols)) return rc;
-  if (!(eps >= 0) || !isfinite(eps)) return fail(ZERO_ERR_INVALID_ARG, "eps = %g", eps);
+  const float eps32 = static_cast<float>(eps);  // what the kernels add
+  if (!(eps >= 0) || !isfinite(eps32) || (eps > 0 && eps32 == 0))
+    return fail(ZERO_ERR_INVALID_ARG, "eps = %g is not 0 or a positive fp32 value", eps);
   if (int rc = check_rows("x", x, dt, rows, cols, x_ld)) return rc;
   if (int rc = check_rows("y", y, dt, rows, cols, y_ld)) return rc;
   if ((mean == nullptr) != (rstd == nullptr)) return fail(ZERO_ERR_INVALID_ARG, "mean and rstd must be given together");
@@ -96,7 +98,7 @@ int zero_layer_norm(const void* x, int32_t dt, int64_t rows, int64_t cols, int64
   N.weight = weight;
   N.bias = bias;
   N.w_dt = w_dt;
-  N.eps = static_cast<float>(eps);
+  N.eps = eps32;
   N.mean = mean;
   N.rstd = rstd;
   hipError_t e = launch_norm(N, dt, static_cast<hipStream_t>(stream));
