@@ -412,3 +412,12 @@ def test_small_values_of_far_gates(act, lo, hi, ws):
         odd = torch.arange(f, device=DEV) % 2 == 1
         mixed, alone = forward(torch.where(odd, gate[0], near)), forward(near)
         assert torch.equal(mixed[:, ~odd], alone[:, ~odd])
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("size", [(700, 1280, 5120), (153, 1344, 7920), (1410, 1584, 1504), (4096, 1024, 1024), (2001, 400, 264)],
+                         ids=str)
+def test_backward_at_sizes_on_both_sides_of_the_shared_launch(size, dt, ws):
+    """Shared launches with dx in splits and with large, middle and small tiles for dw alone; and sizes beside them that
+    take two launches (the last two)."""
+    test_both_products_of_the_backward_pass_in_one_launch(size, dt, ws)

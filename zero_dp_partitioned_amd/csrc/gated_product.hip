@@ -13,6 +13,7 @@
 #include <atomic>
 #include <type_traits>
 
+#include "gated_route.h"
 #include "layer_device.h"
 
 namespace zdp {
@@ -23,15 +24,12 @@ typedef short s8 __attribute__((ext_vector_type(8)));
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 
-enum Use { kForward, kDx, kDw };
-
 // How operands reach LDS: kDirect by fetches that write it themselves (every
 // 16-byte slot of the operands aligned and whole), kStaged through registers
 // (aligned to elements), kMasked value by value (a dimension smaller than the tile).
 enum Fetch { kDirect, kStaged, kMasked };
 
 constexpr int kFrag = 16;      // rows of an operand per instruction
-constexpr int kChunk = 64;     // contraction per stage: 128 bytes of a row
 constexpr int kSteps = 2;      // of 32, per chunk
 constexpr int kPiece = 1024;   // bytes that a wave moves at a time
 constexpr int kPieceRows = 8;  // rows, or as much of the contraction as a piece's columns leave, of a piece
@@ -168,8 +166,6 @@ __device__ __forceinline__ void fetch_to_lds_if(uint32_t i, uint32_t n, const ch
 // Tiles dealt to the eight XCDs (block b runs on XCD b % 8) in contiguous
 // runs, and inside a run in columns of kGroup tile rows, so that the tiles that
 // an XCD's 32 CUs work on at a time share their operands in its L2.
-constexpr int kXcds = 8;
-
 template <uint32_t kGroup>
 __device__ __forceinline__ void tile_of(uint32_t b, uint32_t tm, uint32_t tn, uint32_t* m, uint32_t* n) {
   const uint32_t total = tm * tn, q = total / kXcds, rem = total % kXcds;
@@ -872,9 +868,7 @@ hipError_t tile_launch(const ProductArgs& a, hipStream_t s) {
 
 bool aligned16(const void* p, int64_t ld_bytes) { return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(ld_bytes)) & 15) == 0; }
 
-constexpr int64_t kEnoughTiles = 160;
-constexpr int64_t kCus = 256;
-constexpr int64_t kMostCus = 208;
+constexpr int64_t kScratchFloats = kScratchBytes / sizeof(float);
 constexpr int64_t kFewSmall = 448;
 constexpr int64_t kVeryFew = 128;
 
@@ -920,53 +914,29 @@ hipError_t product_launch(ProductArgs a, float* scratch, hipStream_t s) {
   }
   auto tiles = [&](int64_t tm, int64_t tn) { return ceil_div(a.m, tm) * ceil_div(a.n, tn) * kOutputs; };
   constexpr int kHalf = USE == kForward ? 2 : 1;
-  // a tile has more than half its rows and columns to do; along the columns it must fit its operand
-  auto fits = [&](int64_t side) {
-    return a.m > (USE == kDw ? side - 1 : side / 2) && a.n > (USE != kForward ? side - 1 : side / kHalf / 2);
-  };
-  a.splits = 1;
-  a.partial = nullptr;
-  // By rounds over the CUs: a round of one 256 x 256 tile a CU takes as long as 1.5
-  // rounds of two 128 x 128 tiles a CU, and a round of one of those half of that.
-  // (us, large and middle tiles: forward of 1001 x 1600 x 6400, 200 and 800 tiles: 40,
-  // 50; of 2048 x 4096 x 14336, 896 and 3584: 413, 494; dx of 2048 x 4096 x 14336, 128
-  // and 512: 640, 479.)
-  const int64_t large = ceil_div(tiles(256, 256 / kHalf), kCus) * 6, pairs = ceil_div(tiles(128, 128 / kHalf), 2 * kCus) * 4;
-  if (fits(256) && (!fits(128) || large <= (tiles(128, 128 / kHalf) <= kCus ? 2 : pairs))) {
+  const Route route = route_of(USE, a.m, a.n, a.k, kScratchFloats);
+  const bool middle = route.tile == Route::kMiddle;
+  a.splits = static_cast<int32_t>(route.splits);
+  a.partial = a.splits > 1 ? scratch : nullptr;
+  if (route.tile == Route::kLarge) {
     if constexpr (USE == kForward) return fetch_launch<USE, 4, 8, 4, 2, 2, 1, DT, ODT>(a, s);
     else return fetch_launch<USE, 8, 4, 2, 4, 2, 1, DT, ODT>(a, s);
-  }
-  const int64_t mid = tiles(128, 128 / kHalf);
-  bool middle = fits(128) && mid >= kEnoughTiles;
-  if constexpr (USE != kForward) {
-    // Few tiles over a long contraction are shared among blocks, as far as the
-    // scratch holds their sums: middle tiles where that gives nearly every CU one (dx
-    // of 256 x 4096 x 14336, 64 tiles in 4 splits: 123 us with small tiles, 87; of 300
-    // rows, 96 in 2: 140 and 159), else small ones, two blocks a CU.
-    const int64_t chunks = ceil_div(a.k, kChunk) * (USE == kDx ? 2 : 1);
-    const int64_t room = static_cast<int64_t>(kScratchBytes / sizeof(float)) / (a.m * a.n * kOutputs);
-    const int64_t most = room < chunks / 4 ? room : chunks / 4;
-    auto shared = [&](int64_t have, int64_t want) { return want / have < most ? want / have : most; };
-    const int64_t one = fits(128) ? shared(mid, kCus) : 0;
-    middle = middle || mid * one > kMostCus;
-    const int64_t splits = middle ? (mid >= kEnoughTiles ? shared(mid, 2 * kCus) : one) : shared(tiles(64, 128), 2 * kCus);
-    if (splits > 1) {
-      a.splits = static_cast<int32_t>(splits);
-      a.partial = scratch;
-    }
   }
   hipError_t e;
   // A middle tile with a CU to itself takes eight waves and keeps three stages in
   // flight; where there are two a CU, four waves and one stage each are as good (dx
   // of 2000 x 2048 x 8000, 256 tiles: 215 us with four waves, 203 with eight, 138
   // with three stages in flight too; forward of 128 x 4096 x 14336, 224: 74, 70, 58).
-  // Very few small tiles of a forward pass, which has no scratch to split over, are
-  // halved, and two groups of waves share the contraction (16 x 8192 x 2048: 47 -> 26.5
-  // us; 64 x 4096 x 4096: 26 -> 17; 64 x 4096 x 14336, 224 tiles: 52.5 against 60).
-  // The small tile has two stages in flight where its blocks do not fill the CUs
-  // (forward of 17 x 4096 x 14336, 224 blocks: 61 -> 47.5 us; dx of 1001 x 1600 x
-  // 6400, 416: 74 -> 65) and one where they do (dx of 16 x 4096 x 14336, 512: 46.5
-  // against 50).
+  // Small tiles of a forward pass, which has no scratch to split over, are halved where
+  // that still leaves a CU no more than one (kVeryFew), and two groups of waves share the
+  // contraction (16 x 8192 x 2048: 47 -> 26.5 us; 64 x 4096 x 4096: 26 -> 17; 64 x 4096 x
+  // 14336, 224 tiles: 52.5 against 60; twelve random sizes each: up to 128 tiles took 37 %
+  // less to 5 % more time, 129 to 300 31 to 75 % more, one 14 % less). The small tile has
+  // two stages in flight where its blocks do not fill the CUs (kFewSmall; forward of
+  // 17 x 4096 x 14336, 224 blocks: 61 -> 47.5 us; dx of 1001 x 1600 x 6400, 416: 74 -> 65;
+  // twelve random sizes each: 34 % less to 12 % more forward, 3 and 12 % less to 1 and
+  // 5 % more in dx and dw) and one where they do, two blocks a CU (dx of 16 x 4096 x
+  // 14336, 512: 46.5 against 50; of 24 random sizes within 2 % but one).
   const int64_t blocks = (middle ? tiles(128, 128 / kHalf) : tiles(64, 128 / kHalf)) * a.splits;
   if constexpr (USE == kForward) {
     if (!middle && blocks <= kVeryFew) return fetch_launch<USE, 4, 2, 1, 2, 4, 2, DT, ODT>(a, s);
@@ -979,44 +949,29 @@ hipError_t product_launch(ProductArgs a, float* scratch, hipStream_t s) {
   return join_launch<ODT>(a, kOutputs, s);
 }
 
-// dx and dw together, if that pays: *done says whether they were launched. By an
-// estimate in which a stage of a middle tile takes 0.55 us, one of a large tile 1.45
-// and its ends 6, and the last blocks run half a large tile past the rest (the whole
-// backward pass, us apart and together, and the estimate's ratio: 1500 x 1600 x 6400
-// 211, 171, 0.75; 2048 rows 237, 224, 0.87; 500 rows 94, 88, 0.88; 1001 rows 142, 139.5,
-// 0.88; 600 x 800 x 3200 42, 47, 0.92; 1000 x 1024 x 4096 64, 70, 1.0).
+// dx and dw together, if that pays: *done says whether they were launched.
 template <int DT, int ODT>
 hipError_t pair_launch(ProductArgs x, ProductArgs w, float* scratch, hipStream_t s, bool* done) {
   using X = Tile<kDx, 2, 4, 4, 2, 4>;
   using W = Tile<kDw, 8, 4, 2, 4, 2>;
   *done = false;
-  if (x.m <= X::kM / 2 || x.n < X::kN || w.m < W::kM || w.n < W::kN || !direct_fetch<kDx>(x) || !direct_fetch<kDw>(w))
-    return hipSuccess;
-  const int64_t tiles_x = ceil_div(x.m, X::kM) * ceil_div(x.n, X::kN), tiles_w = 2 * ceil_div(w.m, W::kM) * ceil_div(w.n, W::kN);
-  if (tiles_x > kCus || tiles_w > 4 * kCus) return hipSuccess;
-  const int64_t chunks = 2 * ceil_div(x.k, kChunk);
-  const int64_t room = static_cast<int64_t>(kScratchBytes / sizeof(float)) / (x.m * x.n);
-  int64_t splits = kCus / tiles_x;
-  splits = splits < room ? splits : room;
-  splits = splits < chunks / 4 ? splits : chunks / 4;
-  splits = splits > 1 ? splits : 1;
-  const double tx = 0.55 * chunks / splits, tw = 1.45 * ceil_div(w.k, kChunk) + 6;
-  const double apart = tx + tw * ceil_div(tiles_w, kCus), together = (tx * tiles_x * splits + tw * tiles_w) / kCus;
-  if (together + 0.5 * tw > 0.9 * apart) return hipSuccess;
+  const PairRoute route = pair_route(x.m, x.n, x.k, kScratchFloats);
+  if (!route.together || !direct_fetch<kDx>(x) || !direct_fetch<kDw>(w)) return hipSuccess;
   *done = true;
-  x.splits = static_cast<int32_t>(splits);
+  x.splits = static_cast<int32_t>(route.splits);
   x.partial = scratch;
   w.splits = 1;
   w.partial = nullptr;
+  static_assert(X::kM == 128 && X::kN == 128 && W::kM == 256 && W::kN == 256, "as pair_route counts them");
   const auto kernel = gated_pair_kernel<DT, ODT>;
   constexpr int kLds = X::kLds > W::kLds ? X::kLds : W::kLds;
   static_assert(X::kThreads == 512 && W::kThreads == 512, "");
   static std::atomic<uint64_t> granted{0};
   if (hipError_t e = grant_lds(kernel, kLds, granted)) return e;
-  const uint32_t of_dx = static_cast<uint32_t>(tiles_x * splits), first = (of_dx + kXcds - 1) / kXcds * kXcds;
-  hipLaunchKernelGGL(kernel, dim3(first + static_cast<uint32_t>(tiles_w)), dim3(512), kLds, s, x, w, of_dx, first);
+  const uint32_t of_dx = static_cast<uint32_t>(route.dx_blocks), first = (of_dx + kXcds - 1) / kXcds * kXcds;
+  hipLaunchKernelGGL(kernel, dim3(first + static_cast<uint32_t>(route.tiles)), dim3(512), kLds, s, x, w, of_dx, first);
   if (hipError_t e = hipGetLastError()) return e;
-  return splits > 1 ? join_launch<DT>(x, 1, s) : hipSuccess;
+  return x.splits > 1 ? join_launch<DT>(x, 1, s) : hipSuccess;
 }
 
 template <int DT>
