@@ -12,6 +12,7 @@ import numpy as np
 import pytest
 import torch
 
+import _gated
 import zero_dp_partitioned_amd as zdp
 from _gpu_helpers import DEV
 
@@ -421,3 +422,18 @@ def test_backward_at_sizes_on_both_sides_of_the_shared_launch(size, dt, ws):
     """Shared launches with dx in splits and with large, middle and small tiles for dw alone; and sizes beside them that
     take two launches (the last two)."""
     test_both_products_of_the_backward_pass_in_one_launch(size, dt, ws)
+
+
+@pytest.mark.parametrize("seed", [3, 4])
+@pytest.mark.parametrize("act", ACTS)
+def test_each_gradient_against_differences(act, seed, ws):
+    """dx, dw_gate and dw_up one by one, in directions in which none can be missing (tests/_gated.py; its check is tested
+    with wrong gradients in test_gated_differences.py)."""
+    host = _gated.inputs(seed)
+    x, wg, wu, dh = (t.to(DEV) for t in host)
+    (m, d), f = x.shape, wg.shape[0]
+    h, gate, up, dg, du = (torch.empty(m, f, dtype=x.dtype, device=DEV) for _ in range(5))
+    zdp.gated_product(x, wg, wu, h, act, gate=gate, up=up)
+    dx, dwg, dwu = torch.empty_like(x), torch.empty(f, d, device=DEV), torch.empty(f, d, device=DEV)
+    zdp.gated_product_backward(dh, x, wg, wu, gate, up, dg, du, ws, dx=dx, dw_gate=dwg, dw_up=dwu, act=act)
+    _gated.check_differences((dx, dwg, dwu), *host, act)
