@@ -437,3 +437,18 @@ def test_each_gradient_against_differences(act, seed, ws):
     dx, dwg, dwu = torch.empty_like(x), torch.empty(f, d, device=DEV), torch.empty(f, d, device=DEV)
     zdp.gated_product_backward(dh, x, wg, wu, gate, up, dg, du, ws, dx=dx, dw_gate=dwg, dw_up=dwu, act=act)
     _gated.check_differences((dx, dwg, dwu), *host, act)
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("size", [(2560, 520, 2048), (2561, 515, 2047), (300, 640, 1300)], ids=str)
+def test_forward_in_large_and_middle_tiles(size, dt):
+    """Random values through the tiles that test_forward's sizes do not reach."""
+    test_forward(size, "silu", dt)
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("size", [(4096, 2560, 520), (4099, 2563, 515), (700, 1280, 5120), (520, 2560, 2056), (300, 1288, 1400)],
+                         ids=str)
+def test_backward_in_large_and_middle_tiles_and_one_launch(size, dt, ws):
+    """Random values through the tiles, and the shared launch of dx and dw, that test_backward's sizes do not reach."""
+    test_backward(size, "gelu_tanh", dt, ws)
