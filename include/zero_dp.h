@@ -535,9 +535,9 @@ int zero_gated_product_backward(const void* dh, int64_t dh_ld, const void* x, in
 
 /* ---- testing --------------------------------------------------------------
  * Not an operation of the pages. Caps the blocks of every streaming launch
- * (update, second pass, averaging, scan, restore, cast, and a layer's operators
- * but for the products' tiles) at max_blocks > 0, on
- * top of each launch's own cap (2^21 tiles per launch; 65,536 blocks for the
+ * (update, second pass, averaging, scan, restore, cast; of a layer's operators
+ * layer norm's two passes over rows, dropout, and the gated product's pass from dh
+ * to dgate and dup) at max_blocks > 0, on top of each launch's own cap (2^21 tiles per launch; 65,536 blocks for the
  * second pass and the scan; 1,024 for the restore). Every streaming kernel
  * loops over the tiles its grid does not cover, so a small shard under a low
  * cap runs the same grid-stride loops that otherwise only shards of billions

@@ -452,3 +452,33 @@ def test_forward_in_large_and_middle_tiles(size, dt):
 def test_backward_in_large_and_middle_tiles_and_one_launch(size, dt, ws):
     """Random values through the tiles, and the shared launch of dx and dw, that test_backward's sizes do not reach."""
     test_backward(size, "gelu_tanh", dt, ws)
+
+
+@pytest.mark.parametrize("cap", [1, 3])
+@pytest.mark.parametrize("pad", [0, 3])
+@pytest.mark.parametrize("dt", DTS)
+def test_backward_under_a_grid_cap(dt, pad, cap, ws):
+    """The gate pass's loop over what its grid does not cover, over dense rows (one run) and strided ones, with dgate and
+    dup of their own and in the place of gate and up: the bits of the free run."""
+    m, d, f = 37, 40, 1601
+    g, dtype = torch.Generator(device=DEV).manual_seed(cap), DTS[dt]
+    x, wg, wu, dh, gate, up = (torch.randn(*s, generator=g, device=DEV).to(dtype)
+                               for s in ((m, d), (f, d), (f, d), (m, f), (m, f), (m, f)))
+
+    def run(own):
+        a, b, c = (wide(t.clone(), pad) for t in (dh, gate, up))
+        dg, du = (Blank(m, f, dtype, pad), Blank(m, f, dtype, pad)) if own else (None, None)
+        dx, dwg, dwu = torch.empty_like(x), torch.empty_like(wg), torch.empty_like(wu)
+        p, q = (dg.t, du.t) if own else (b, c)
+        zdp.gated_product_backward(a, x, wg, wu, b, c, p, q, ws, dx=dx, dw_gate=dwg, dw_up=dwu, act="silu")
+        if own:
+            dg.check()
+            du.check()
+        return [t.clone() for t in (p, q, dx, dwg, dwu)]
+    free = run(True)
+    zdp.set_grid_limit(cap)
+    try:
+        capped, over = run(True), run(False)
+    finally:
+        zdp.set_grid_limit(0)
+    assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(free, capped, over))
