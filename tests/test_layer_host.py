@@ -2,6 +2,8 @@
 the binding) fire before anything touches a device, and the plain forms the GPU
 tests compare with are the published generator and the formulas' derivatives."""
 import inspect
+import os
+import re
 
 import numpy as np
 import pytest
@@ -9,6 +11,7 @@ import torch
 
 import _layer
 import zero_dp_partitioned_amd as zdp
+from zero_dp_partitioned_amd import build
 
 A = 1 << 20  # an aligned address that is never read: the checks come first
 BIG = 2 ** 62
@@ -295,3 +298,17 @@ def test_the_norm_s_gradient_is_its_slope():
     up, down = (_layer.norm(x + s * h * e[0], w + s * h * e[1], b + s * h * e[2], 1e-5)[0] for s in (1, -1))
     slope = ((up - down) / (2 * h) * dy).sum()
     assert abs((dx * e[0]).sum() + (dw * e[1]).sum() + (db * e[2]).sum() - slope) < 1e-7
+
+
+def test_the_pieces_that_both_products_keep_are_the_same():
+    """gated_product.hip and mx_product.hip each deal tiles to the XCDs and fetch to LDS in asm of their own: a change to
+    one is a change to both, but for the operands' type."""
+    def pieces(name):
+        with open(os.path.join(build.CSRC, name)) as f:
+            text = f.read()
+        deal = re.search(r"void tile_of\([^{]*\{\n(.*?)^\}", text, re.S | re.M)[1]
+        fetch = re.search(r"void fetch_to_lds_if\([^{]*\{\n(.*?)^\}", text, re.S | re.M)[1]
+        grant = re.search(r"  int dev = 0;\n(.*?granted\.fetch_or[^\n]*\n  \}\n)", text, re.S)[1]
+        return deal, fetch, grant
+    for mine, other in zip(pieces("gated_product.hip"), pieces("mx_product.hip")):
+        assert mine == other
