@@ -521,10 +521,12 @@ int zero_gated_product(const void* x, int32_t dt, int64_t m, int64_t d, int64_t 
  * left:
  *   dgate = dh * act'(gate) * up,   dup = dh * act(gate)   (m x f),
  *   dx = dgate w_gate + dup w_up,   dw_gate = dgate^T x,   dw_up = dup^T x.
- * dgate and dup are rounded to x's type, and the products are those of the rounded
- * values (fp32 sums). They may be gate and up themselves (the same addresses and
- * ld), which are not read again. dx may be NULL (then w_gate and w_up may be), and
- * so may dw_gate and dw_up together (then x may be); these are of dw_dt (x's type
+ * dgate and dup are rounded to x's type (in fp16 infinite past 65504, which reaches
+ * the step's overflow flag through dw, and 0 below 2^-25), and the products are
+ * those of the rounded values (fp32 sums). Finite gates give finite derivatives;
+ * infinite ones may give NaN, as 0 * infinity in the formulas does. dgate and dup
+ * may be gate and up themselves (the same addresses and ld), which are not read
+ * again. dx may be NULL (then w_gate and w_up may be), and so may dw_gate and dw_up together (then x may be); these are of dw_dt (x's type
  * or F32, dw_ld from row to row), and accumulate != 0 adds them to what they hold.
  * Errors: as zero_gated_product; WORKSPACE. */
 int zero_gated_product_backward(const void* dh, int64_t dh_ld, const void* x, int32_t dt, int64_t m, int64_t d,

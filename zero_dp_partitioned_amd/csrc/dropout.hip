@@ -9,7 +9,7 @@
 namespace zdp {
 namespace {
 
-constexpr int kSlots = 2;  // 16-byte slots a lane handles, all loads first (four: 71 us instead of 69 below, one: 70)
+constexpr int kSlots = 2;  // 16-byte slots a lane handles, all loads first (four took 3 % more time at 16384 x 4096 bf16, one 1 %)
 // Tensors from 64 MiB on are read with the non-temporal hint (16384 x 4096 bf16
 // with a residual: 75 -> 71 us; 8192 x 1600 fp16, which the caches hold: 17.1 -> 18.2).
 constexpr int64_t kOnceSlots = (64 << 20) / 16;

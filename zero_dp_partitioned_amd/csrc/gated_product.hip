@@ -259,7 +259,7 @@ __device__ __forceinline__ uint32_t tiles_of(int64_t n, uint32_t size) { return 
 // block fills a CU; more blocks of the smaller ones.
 //
 // What bounds the large tile (256 x 256, eight waves of 128 x 64 or 64 x 128) is
-// power: 8192 x 4096 x 14336 in bf16 takes 1395-1470 us (1.31-1.38 PFLOP/s), dx
+// power: 8192 x 4096 x 14336 in bf16 takes 1375-1470 us (1.31-1.40 PFLOP/s), dx
 // 1340-1410, dw 1380-1430 on several cards, at 1.5-1.9 GHz; with the wait for
 // fetches left out it took 1-2 % less. The instruction alone reaches 2.08 PFLOP/s on
 // such values (32 x 32 x 16: 1.83, and the kernel was 2-3 % slower with it). Four
@@ -801,8 +801,12 @@ __global__ void __launch_bounds__(256) gated_join_kernel(const ProductArgs P, in
 }
 
 // ------------------------------------------------------------------------
-// dg = dh act'(g) u, du = dh act(g): a streaming pass, 8192 x 14336 in bf16 195 us
-// (6.0 TB/s). dg and du may lie where g and u do.
+// dg = dh act'(g) u, du = dh act(g): a streaming pass, 8192 x 14336 in bf16 196 us
+// (6.0 TB/s). dg and du may lie where g and u do. They are rounded to the operands'
+// type because the products that follow take no other on the matrix pipes: as
+// two 16-bit terms each they would double the products' time. dx and dw are then 1.4 times as far from the
+// formula as their own rounding makes them (2.3e-3 in bf16, 2.9e-4 in fp16, in the
+// 2-norm), and what passes fp16's range is infinite, as any fp16 gradient is.
 // ------------------------------------------------------------------------
 
 struct GateGradArgs {
@@ -930,7 +934,7 @@ hipError_t product_launch(ProductArgs a, float* scratch, hipStream_t s) {
   // Small tiles of a forward pass, which has no scratch to split over, are halved where
   // that still leaves a CU no more than one (kVeryFew), and two groups of waves share the
   // contraction (16 x 8192 x 2048: 47 -> 26.5 us; 64 x 4096 x 4096: 26 -> 17; 64 x 4096 x
-  // 14336, 224 tiles: 52.5 against 60; twelve random sizes each: up to 128 tiles took 37 %
+  // 14336, 224 tiles: 14 % more; twelve random sizes each: up to 128 tiles took 37 %
   // less to 5 % more time, 129 to 300 31 to 75 % more, one 14 % less). The small tile has
   // two stages in flight where its blocks do not fill the CUs (kFewSmall; forward of
   // 17 x 4096 x 14336, 224 blocks: 61 -> 47.5 us; dx of 1001 x 1600 x 6400, 416: 74 -> 65;

@@ -117,8 +117,8 @@ struct Slot {
 // W waves a row, V 16-byte slots a lane; a block of one wave a row has four
 // rows. At least Vec<DT>::kVals columns. Measured: 16384 x 4096 bf16 50 us (5.4
 // TB/s), 8192 x 1600 fp16 12.7 (4.1), one row of 4096 3.0 in a graph. The output
-// goes past the caches, the input does not: with the hint on both the first took
-// 50.6 us and the second 13.9 instead of 13.3.
+// goes past the caches, the input does not: with the hint on both the first took 1 %
+// more and the second, which the caches hold, 4 %.
 template <int DT, int V, int W>
 __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) norm_kernel(const NormArgs N) {
   constexpr int kVals = Vec<DT>::kVals, kElem = Vec<DT>::kElem, kRows = W == 1 ? 4 : 1;
@@ -249,8 +249,8 @@ __host__ __device__ inline int64_t sums_pitch(int64_t cols) { return (cols + 3) 
 // leaves one row of sums. The next row's loads are in flight while a row is
 // worked on. A block's groups take equally many turns, so that its barriers meet.
 // Measured, 16384 x 4096 bf16 with dresidual: 91-92 us (5.8-5.9 TB/s) and 4.6 for
-// the join; two blocks a CU instead of one are no faster there and 33 us instead of
-// 30 at 8192 x 1600. All of it goes past the caches (115 -> 107 us).
+// the join; two blocks a CU instead of one are no faster there and 10 % slower
+// at 8192 x 1600 fp16 (28 us with the join, 29 with dresidual). All of it goes past the caches (115 -> 107 us).
 template <int DT, int V, int W, int G, bool RES>
 __global__ void __launch_bounds__(64 * W * G, 2) norm_grad_kernel(const NormGradArgs N) {
   constexpr int kVals = Vec<DT>::kVals, kElem = Vec<DT>::kElem;
@@ -507,7 +507,7 @@ hipError_t norm_launch(const NormArgs& a, hipStream_t s) {
   if (a.cols >= Vec<DT>::kVals) {
     if (slots <= 64) return norm_start<DT, 1, 1>(a, s);
     if (slots <= 128) return norm_start<DT, 2, 1>(a, s);
-    if (slots <= 256) return norm_start<DT, 2, 2>(a, s);  // one wave with four slots: 13.3 us at 8192 x 1600 fp16, 12.4
+    if (slots <= 256) return norm_start<DT, 2, 2>(a, s);  // one wave with four slots: 7 % more at 8192 x 1600 fp16
     if (slots <= 512) return norm_start<DT, 2, 4>(a, s);
     if (slots <= 1024) return norm_start<DT, 4, 4>(a, s);
     if (slots <= 2048) return norm_start<DT, 4, 8>(a, s);
