@@ -44,35 +44,20 @@ __device__ __forceinline__ float row_sum(float x, float* part, int w, int lane) 
   return x;
 }
 
-// Rows whose sums pass fp32's range, though their values do not: the sums are
-// formed again from values times a power of two, and the results scaled back. (Sums of
-// both signs may have come to NaN.) Every wave of a row gets here or none does.
-// `again(scale)` gives this lane's share of the scaled sum. A row whose distances
-// from the mean pass the range too, or that holds an infinity or NaN, is NaN.
+// Rows whose sums pass fp32's range, though their values do not, are worked out
+// again (kScaled) from values times a power of two, and the results scaled back. What
+// sends them there is a sum of squares that is not finite, as it is too if the mean
+// was not. Every wave of a row goes or none does. A row whose distances from the mean
+// pass the range too, or that holds an infinity or NaN, is NaN.
 constexpr float kMeanScale = 0x1p-20f;    // 2^20 values below 2^128
 constexpr float kSquareScale = 0x1p-76f;  // 2^20 squares of values below 2^128
+using Plain = std::false_type;
+using Scaled = std::true_type;
 
-template <int W, typename Again>
-__device__ __forceinline__ float row_sum_scaled(float scale, float* part, int w, int lane, Again&& again) {
-  if constexpr (W > 1) __syncthreads();  // `part` has been read
-  const float s = row_sum<W>(again(scale), part, w, lane);
-  if constexpr (W > 1) __syncthreads();
-  return s;
-}
+__device__ __forceinline__ float rstd_of(float sq, float inv, float eps) { return 1.0f / sqrtf(sq * inv + eps); }
 
-template <int W, typename Again>
-__device__ __forceinline__ float row_mean(float sum, float inv, float* part, int w, int lane, Again&& again) {
-  sum = row_sum<W>(sum, part, w, lane);
-  if (__builtin_isfinite(sum)) return sum * inv;
-  return row_sum_scaled<W>(kMeanScale, part, w, lane, again) * inv * (1.f / kMeanScale);
-}
-
-template <int W, typename Again>
-__device__ __forceinline__ float row_rstd(float sq, float inv, float eps, float* part, int w, int lane, Again&& again) {
-  sq = row_sum<W>(sq, part, w, lane);
-  if (!__builtin_isinf(sq)) return 1.0f / sqrtf(sq * inv + eps);
-  sq = row_sum_scaled<W>(kSquareScale, part, w, lane, again);
-  return 1.0f / sqrtf(sq * inv + eps * kSquareScale * kSquareScale) * kSquareScale + (sq - sq);  // NaN for infinity
+__device__ __forceinline__ float rstd_of_scaled(float sq, float inv, float eps) {
+  return rstd_of(sq, inv, eps * kSquareScale * kSquareScale) * kSquareScale + (sq - sq);  // NaN for infinity
 }
 
 // Vec<DT>::kVals values of the weight (or bias), of x's type or fp32, from column `col` on.
@@ -128,41 +113,43 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) norm_kernel(const NormA
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + (W == 1 ? wave : 0); row < N.rows;
        row += static_cast<int64_t>(gridDim.x) * kRows) {
     const char* const x = static_cast<const char*>(N.x.p) + row * N.x.ld * kElem;
-    float v[V][kVals];
-    u4 raw[V];
+    float v[V][kVals], mean;
+    // the row's values less their mean; the sum of their squares
+    auto center = [&](auto scaled) {
+      constexpr bool kScaled = decltype(scaled)::value;
+      int lane = threadIdx.x & 63;
+      // slots of its own: the rare path holds no registers through the other (two slots of
+      // 16 bits: 83 registers, and 65536 x 1000 4-5 % slower; more waves a row do better without)
+      if (kScaled && W == 1) asm("" : "+v"(lane));
+      u4 raw[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) raw[j] = Slot<DT, W>(j, w, lane, N.cols).load(x);
-#pragma unroll
-    for (int j = 0; j < V; ++j) widen<DT>(raw[j], v[j]);
-    auto share = [&](float scale) {
+      for (int j = 0; j < V; ++j) raw[j] = Slot<DT, W>(j, w, lane, N.cols).load(x);
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const Slot<DT, W> slot(j, w, lane, N.cols);
+        widen<DT>(raw[j], v[j]);
 #pragma unroll
-        for (int e = 0; e < kVals; ++e) sum += e >= slot.skip ? v[j][e] * scale : 0.f;
+        for (int e = 0; e < kVals; ++e) sum += e >= slot.skip ? (kScaled ? v[j][e] * kMeanScale : v[j][e]) : 0.f;
       }
-      return sum;
-    };
-    const float mean = row_mean<W>(share(1.f), inv, part, w, lane, share);
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-#pragma unroll
-      for (int e = 0; e < kVals; ++e) v[j][e] -= mean;
-    auto squares = [&](float scale) {
+      mean = row_sum<W>(sum, part, w, lane) * inv;
+      if (kScaled) mean *= 1.f / kMeanScale;
       float sq = 0.f;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const Slot<DT, W> slot(j, w, lane, N.cols);
 #pragma unroll
         for (int e = 0; e < kVals; ++e) {
-          const float d = e >= slot.skip ? v[j][e] * scale : 0.f;
+          v[j][e] -= mean;
+          const float d = e >= slot.skip ? (kScaled ? v[j][e] * kSquareScale : v[j][e]) : 0.f;
           sq = __builtin_fmaf(d, d, sq);
         }
       }
-      return sq;
+      return row_sum<W>(sq, part + W, w, lane);
     };
-    const float rstd = row_rstd<W>(squares(1.f), inv, N.eps, part + W, w, lane, squares);
+    const float sq = center(Plain{});
+    float rstd = rstd_of(sq, inv, N.eps);
+    if (!__builtin_isfinite(sq)) rstd = rstd_of_scaled(center(Scaled{}), inv, N.eps);
     if (N.mean && lane == 0 && w == 0) {
       N.mean[row] = mean;
       N.rstd[row] = rstd;
@@ -202,25 +189,27 @@ __global__ void __launch_bounds__(kLongThreads) norm_long_kernel(const NormArgs 
         f(col, v);
       }
     };
-    auto share = [&](float scale) {
+    float mean;
+    auto squares = [&](auto scaled) {
+      constexpr bool kScaled = decltype(scaled)::value;
       float sum = 0.f;
       each([&](int, const float* v) {
-        for (int e = 0; e < kVals; ++e) sum += v[e] * scale;
+        for (int e = 0; e < kVals; ++e) sum += kScaled ? v[e] * kMeanScale : v[e];
       });
-      return sum;
-    };
-    const float mean = row_mean<kWaves>(share(1.f), inv, part, w, lane, share);
-    auto squares = [&](float scale) {
+      mean = row_sum<kWaves>(sum, part, w, lane) * inv;
+      if (kScaled) mean *= 1.f / kMeanScale;
       float sq = 0.f;
       each([&](int col, const float* v) {
         for (int e = 0; e < kVals; ++e) {
-          const float d = col + e < N.cols ? (v[e] - mean) * scale : 0.f;
+          const float d = col + e < N.cols ? (kScaled ? (v[e] - mean) * kSquareScale : v[e] - mean) : 0.f;
           sq = __builtin_fmaf(d, d, sq);
         }
       });
-      return sq;
+      return row_sum<kWaves>(sq, part + kWaves, w, lane);
     };
-    const float rstd = row_rstd<kWaves>(squares(1.f), inv, N.eps, part + kWaves, w, lane, squares);
+    const float sq = squares(Plain{});
+    float rstd = rstd_of(sq, inv, N.eps);
+    if (!__builtin_isfinite(sq)) rstd = rstd_of_scaled(squares(Scaled{}), inv, N.eps);
     if (N.mean && threadIdx.x == 0) {
       N.mean[row] = mean;
       N.rstd[row] = rstd;
