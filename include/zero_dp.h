@@ -468,7 +468,8 @@ int zero_mx_product(const void* a_codes, const void* a_scales, int64_t lda, cons
  * fp32 reaches. Rows of no values leave y, mean and rstd as they are.
  * weight and bias have `cols` values of w_dt: x's type or F32; bias may be NULL.
  * mean and rstd (fp32, one a row, what the backward pass reads) are written unless
- * both are NULL. eps is 0 or rounds to a positive fp32 value.
+ * both are NULL. eps is at most fp32's largest value; one below its smallest counts as
+ * that, and 0 as 0 (a row without spread is then NaN).
  * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (more than 2^20 columns). */
 int zero_layer_norm(const void* x, int32_t dt, int64_t rows, int64_t cols, int64_t x_ld, const void* weight,
                     const void* bias, int32_t w_dt, double eps, void* y, int64_t y_ld, float* mean, float* rstd,

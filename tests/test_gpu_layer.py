@@ -202,6 +202,19 @@ def test_an_infinite_gradient_at_a_row_s_end(cols, dt):
     assert dw[:cols - 1].isfinite().all() and db[cols - 1] == float("inf")
 
 
+@pytest.mark.parametrize("eps", [1e-45, 1e-46, 1e-300, 5e-324])
+def test_norm_with_an_eps_below_fp32_s_values(eps):
+    """It still keeps rows without spread from NaN, and adds nothing to the others."""
+    x = torch.zeros(4, 100, device=DEV)
+    x[1] = 3.25
+    x[2:] = torch.randn(2, 100, device=DEV)
+    w, b = torch.full((100,), 2.0, device=DEV), torch.full((100,), 0.5, device=DEV)
+    y, plain = torch.empty_like(x), torch.empty_like(x)
+    zdp.layer_norm(x, w, b, y, eps)
+    zdp.layer_norm(x, w, b, plain, 0.0)
+    assert (y[:2] == 0.5).all() and torch.equal(y[2:], plain[2:]) and plain[:2].isnan().all()
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("cols", [3, 5, 64, 1000, 1600, 4096, 9000, 33000])
 def test_norm_of_rows_whose_sums_pass_fp32(cols, dt):

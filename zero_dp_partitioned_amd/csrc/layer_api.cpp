@@ -1,4 +1,5 @@
 // Host side of a layer's operators (include/zero_dp.h): argument checks and launches.
+#include <float.h>
 #include <hip/hip_runtime.h>
 #include <math.h>
 
@@ -78,9 +79,9 @@ int zero_layer_norm(const void* x, int32_t dt, int64_t rows, int64_t cols, int64
                     const void* bias, int32_t w_dt, double eps, void* y, int64_t y_ld, float* mean, float* rstd,
                     void* stream) {
   if (int rc = check_norm(dt, w_dt, rows, cols)) return rc;
-  const float eps32 = static_cast<float>(eps);  // what the kernels add
-  if (!(eps >= 0) || !isfinite(eps32) || (eps > 0 && eps32 == 0))
-    return fail(ZERO_ERR_INVALID_ARG, "eps = %g is not 0 or a positive fp32 value", eps);
+  if (!(eps >= 0) || !(eps <= FLT_MAX)) return fail(ZERO_ERR_INVALID_ARG, "eps = %g", eps);
+  // what the kernels add: not 0 for a smaller eps, which would make a row without spread NaN
+  const float eps32 = eps > 0 && eps < FLT_TRUE_MIN ? FLT_TRUE_MIN : static_cast<float>(eps);
   if (int rc = check_rows("x", x, dt, rows, cols, x_ld)) return rc;
   if (int rc = check_rows("y", y, dt, rows, cols, y_ld)) return rc;
   if ((mean == nullptr) != (rstd == nullptr)) return fail(ZERO_ERR_INVALID_ARG, "mean and rstd must be given together");
