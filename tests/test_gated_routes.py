@@ -22,6 +22,8 @@ MEASURED = {
     (153, 3344, 7920): (119.1, 100.0), (1470, 1720, 6536): (247.5, 187.1), (1500, 1608, 1000): (52.3, 45.8),
     (2079, 1000, 3776): (132.5, 91.1), (1408, 1584, 1504): (69.9, 44.9), (3267, 584, 3600): (159.2, 105.3),
     (2550, 1024, 2856): (119.4, 82.3), (647, 3408, 608): (38.3, 28.8), (474, 4216, 504): (34.0, 24.5),
+    (2960, 344, 19952): (391.4, 350.9), (1576, 776, 17120): (376.0, 312.6), (2787, 1088, 13440): (481.3, 453.2),
+    (3159, 384, 19256): (385.0, 410.0), (1031, 2712, 520): (37.5, 49.6), (1648, 312, 3392): (56.2, 74.7),
     (2118, 1088, 1032): (55.1, 57.3), (256, 4096, 4096): (65.7, 65.3), (8033, 328, 17136): (930.4, 820.4),
 }
 

@@ -99,11 +99,13 @@ inline PairRoute pair_route(int64_t m, int64_t d, int64_t f, int64_t room) {
   if (w.splits > 1) return r;
   // Between the two, by when the last block ends: a stage of a middle tile takes 0.55
   // us, one of a large tile 1.45 and its ends 6, a launch 2. An XCD's 32 CUs take its
-  // share of dx's blocks first, then of dw's. Below three quarters 51 sizes took from
-  // 4 % more to 36 % less time together (2079 x 1000 x 3776 133, 91; 1500 x 1608 x 1000
-  // 52, 46; 2118 x 1088 x 1032 55, 57), above it 12 sizes from as long to 34 % more (1500
-  // x 1600 x 640 38, 43; 2048 x 768 x 3000 87, 99; 3953 x 672 x 2624, where an XCD gets
-  // one block too many, 111, 149).
+  // share of dx's blocks first, then of dw's. Of sizes with a round of dw's tiles at
+  // most, 59 that end within three quarters of the time apart took from 4 % more to
+  // 36 % less together (2079 x 1000 x 3776 133, 91; 1500 x 1608 x 1000 52, 46; 2118 x 1088 x
+  // 1032 55, 57), 74 others from 6 % less to 34 % more (1500 x 1600 x 640 38, 43; 2048 x
+  // 768 x 3000 87, 99; 3953 x 672 x 2624, where an XCD gets one block too many, 111,
+  // 149). With more than a round 13 up to 0.84 took as long to 26 % less (2960 x 344 x
+  // 19952 391, 351), three above it 6 % more.
   const double tx = 0.55 * chunks / r.splits, tw = 1.45 * tiles_over(m, kChunk) + 6;
   const int64_t cus = kCus / kXcds, busy = tiles_over(r.dx_blocks, kXcds);
   double idle_from = 0, dx_from = tx, end = tx;
@@ -114,7 +116,7 @@ inline PairRoute pair_route(int64_t m, int64_t d, int64_t f, int64_t room) {
     from += tw;
     end = end > from ? end : from;
   }
-  r.together = end <= 0.75 * (tx + tw * tiles_over(r.tiles, kCus) + 2);
+  r.together = end <= (r.tiles > kCus ? 0.85 : 0.75) * (tx + tw * tiles_over(r.tiles, kCus) + 2);
   return r;
 }
 
