@@ -100,6 +100,9 @@ int zero_layer_norm(const void* x, int32_t dt, int64_t rows, int64_t cols, int64
   N.bias = bias;
   N.w_dt = w_dt;
   N.eps = eps32;
+  N.inv = 1.0f / static_cast<float>(cols);
+  N.scale = ldexpf(1.0f, ilogbf(N.inv) - 1);  // (one power to spare for the sum's roundings)
+  N.unscale = N.inv / N.scale;
   N.mean = mean;
   N.rstd = rstd;
   hipError_t e = launch_norm(N, dt, static_cast<hipStream_t>(stream));

@@ -44,20 +44,15 @@ __device__ __forceinline__ float row_sum(float x, float* part, int w, int lane) 
   return x;
 }
 
-// Rows whose sums pass fp32's range, though their values do not, are worked out
-// again (kScaled) from values times a power of two, and the results scaled back. What
-// sends them there is a sum of squares that is not finite, as it is too if the mean
-// was not. Every wave of a row goes or none does. A row whose distances from the mean
-// pass the range too, or that holds an infinity or NaN, is NaN.
-constexpr float kMeanScale = 0x1p-20f;    // 2^20 values below 2^128
-constexpr float kSquareScale = 0x1p-76f;  // 2^20 squares of values below 2^128
-using Plain = std::false_type;
-using Scaled = std::true_type;
+// A row's sums may pass fp32's range though its values do not. Its mean is summed
+// from values times a power of two below 1 / cols, which changes no bit of it (but for
+// values under 2^-126 times cols, by less than 2^-148 times cols). Its squares are summed as they are and, if that sum is not finite, once more from
+// distances times kFar; every wave of a row does that or none does. If they pass the
+// range then too, the row is NaN.
+constexpr float kFar = 0x1p-76f;  // 2^20 squares of values below 2^128
 
-__device__ __forceinline__ float rstd_of(float sq, float inv, float eps) { return 1.0f / sqrtf(sq * inv + eps); }
-
-__device__ __forceinline__ float rstd_of_scaled(float sq, float inv, float eps) {
-  return rstd_of(sq, inv, eps * kSquareScale * kSquareScale) * kSquareScale + (sq - sq);  // NaN for infinity
+__device__ __forceinline__ float rstd_of_far(float sq, float inv, float eps) {
+  return 1.0f / sqrtf(sq * inv + eps * kFar * kFar) * kFar + (sq - sq);  // NaN for infinity
 }
 
 // Vec<DT>::kVals values of the weight (or bias), of x's type or fp32, from column `col` on.
@@ -109,47 +104,49 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) norm_kernel(const NormA
   constexpr int kVals = Vec<DT>::kVals, kElem = Vec<DT>::kElem, kRows = W == 1 ? 4 : 1;
   __shared__ float part[2 * W];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, w = W == 1 ? 0 : wave;
-  const float inv = 1.0f / static_cast<float>(N.cols);
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + (W == 1 ? wave : 0); row < N.rows;
        row += static_cast<int64_t>(gridDim.x) * kRows) {
     const char* const x = static_cast<const char*>(N.x.p) + row * N.x.ld * kElem;
-    float v[V][kVals], mean;
-    // the row's values less their mean; the sum of their squares
-    auto center = [&](auto scaled) {
-      constexpr bool kScaled = decltype(scaled)::value;
-      int lane = threadIdx.x & 63;
-      // slots of its own: the rare path holds no registers through the other (two slots of
-      // 16 bits: 83 registers, and 65536 x 1000 4-5 % slower; more waves a row do better without)
-      if (kScaled && W == 1) asm("" : "+v"(lane));
-      u4 raw[V];
+    float v[V][kVals];
+    u4 raw[V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) raw[j] = Slot<DT, W>(j, w, lane, N.cols).load(x);
-      float sum = 0.f;
+    for (int j = 0; j < V; ++j) raw[j] = Slot<DT, W>(j, w, lane, N.cols).load(x);
+    float sum = 0.f;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const Slot<DT, W> slot(j, w, lane, N.cols);
-        widen<DT>(raw[j], v[j]);
+    for (int j = 0; j < V; ++j) {
+      const Slot<DT, W> slot(j, w, lane, N.cols);
+      widen<DT>(raw[j], v[j]);
 #pragma unroll
-        for (int e = 0; e < kVals; ++e) sum += e >= slot.skip ? (kScaled ? v[j][e] * kMeanScale : v[j][e]) : 0.f;
+      for (int e = 0; e < kVals; ++e) sum = __builtin_fmaf(e >= slot.skip ? v[j][e] : 0.f, N.scale, sum);
+    }
+    const float mean = row_sum<W>(sum, part, w, lane) * N.unscale;
+    float sq = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const Slot<DT, W> slot(j, w, lane, N.cols);
+#pragma unroll
+      for (int e = 0; e < kVals; ++e) {
+        v[j][e] -= mean;
+        const float d = e >= slot.skip ? v[j][e] : 0.f;
+        sq = __builtin_fmaf(d, d, sq);
       }
-      mean = row_sum<W>(sum, part, w, lane) * inv;
-      if (kScaled) mean *= 1.f / kMeanScale;
-      float sq = 0.f;
+    }
+    sq = row_sum<W>(sq, part + W, w, lane);
+    float rstd = 1.0f / sqrtf(sq * N.inv + N.eps);
+    if (__builtin_expect(!__builtin_isfinite(sq), 0)) {
+      sq = 0.f;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const Slot<DT, W> slot(j, w, lane, N.cols);
 #pragma unroll
         for (int e = 0; e < kVals; ++e) {
-          v[j][e] -= mean;
-          const float d = e >= slot.skip ? (kScaled ? v[j][e] * kSquareScale : v[j][e]) : 0.f;
+          const float d = e >= slot.skip ? v[j][e] * kFar : 0.f;
           sq = __builtin_fmaf(d, d, sq);
         }
       }
-      return row_sum<W>(sq, part + W, w, lane);
-    };
-    const float sq = center(Plain{});
-    float rstd = rstd_of(sq, inv, N.eps);
-    if (!__builtin_isfinite(sq)) rstd = rstd_of_scaled(center(Scaled{}), inv, N.eps);
+      if (W > 1) __syncthreads();  // the sums have been read
+      rstd = rstd_of_far(row_sum<W>(sq, part + W, w, lane), N.inv, N.eps);
+    }
     if (N.mean && lane == 0 && w == 0) {
       N.mean[row] = mean;
       N.rstd[row] = rstd;
@@ -179,7 +176,6 @@ __global__ void __launch_bounds__(kLongThreads) norm_long_kernel(const NormArgs 
   constexpr int kVals = Vec<DT>::kVals, kElem = Vec<DT>::kElem, kWaves = kLongThreads / 64;
   __shared__ float part[2 * kWaves];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const float inv = 1.0f / static_cast<float>(N.cols);
   for (int64_t row = blockIdx.x; row < N.rows; row += gridDim.x) {
     const char* const x = static_cast<const char*>(N.x.p) + row * N.x.ld * kElem;
     auto each = [&](auto&& f) {
@@ -189,27 +185,27 @@ __global__ void __launch_bounds__(kLongThreads) norm_long_kernel(const NormArgs 
         f(col, v);
       }
     };
-    float mean;
-    auto squares = [&](auto scaled) {
-      constexpr bool kScaled = decltype(scaled)::value;
-      float sum = 0.f;
-      each([&](int, const float* v) {
-        for (int e = 0; e < kVals; ++e) sum += kScaled ? v[e] * kMeanScale : v[e];
-      });
-      mean = row_sum<kWaves>(sum, part, w, lane) * inv;
-      if (kScaled) mean *= 1.f / kMeanScale;
+    float sum = 0.f;
+    each([&](int, const float* v) {
+      for (int e = 0; e < kVals; ++e) sum = __builtin_fmaf(v[e], N.scale, sum);
+    });
+    const float mean = row_sum<kWaves>(sum, part, w, lane) * N.unscale;
+    auto squares = [&](float far) {
       float sq = 0.f;
       each([&](int col, const float* v) {
         for (int e = 0; e < kVals; ++e) {
-          const float d = col + e < N.cols ? (kScaled ? (v[e] - mean) * kSquareScale : v[e] - mean) : 0.f;
+          const float d = col + e < N.cols ? (v[e] - mean) * far : 0.f;
           sq = __builtin_fmaf(d, d, sq);
         }
       });
       return row_sum<kWaves>(sq, part + kWaves, w, lane);
     };
-    const float sq = squares(Plain{});
-    float rstd = rstd_of(sq, inv, N.eps);
-    if (!__builtin_isfinite(sq)) rstd = rstd_of_scaled(squares(Scaled{}), inv, N.eps);
+    const float sq = squares(1.f);
+    float rstd = 1.0f / sqrtf(sq * N.inv + N.eps);
+    if (__builtin_expect(!__builtin_isfinite(sq), 0)) {
+      __syncthreads();  // the sums have been read
+      rstd = rstd_of_far(squares(kFar), N.inv, N.eps);
+    }
     if (N.mean && threadIdx.x == 0) {
       N.mean[row] = mean;
       N.rstd[row] = rstd;
