@@ -29,8 +29,10 @@ struct NormArgs {
   const void* bias;  // or null
   int32_t w_dt;      // of weight and bias: x's type or F32
   float eps;
-  float inv, scale, unscale;  // 1 / cols; a power of two below it, and what makes a sum of values times that the mean
-  float* mean;                // one a row, or null (both)
+  float inv;      // 1 / cols
+  float scale;    // a power of two below it
+  float unscale;  // what makes a sum of values times `scale` the mean
+  float* mean;    // one a row, or null (both)
   float* rstd;
 };
 

@@ -46,9 +46,10 @@ __device__ __forceinline__ float row_sum(float x, float* part, int w, int lane) 
 
 // A row's sums may pass fp32's range though its values do not. Its mean is summed
 // from values times a power of two below 1 / cols, which changes no bit of it (but for
-// values under 2^-126 times cols, by less than 2^-148 times cols). Its squares are summed as they are and, if that sum is not finite, once more from
-// distances times kFar; every wave of a row does that or none does. If they pass the
-// range then too, the row is NaN.
+// values under 2^-126 times cols, by less than 2^-148 times cols). Its squares are
+// summed as they are and, if that sum is not finite, once more from distances times
+// kFar; every wave of a row does that or none does. If they pass the range then too,
+// the row is NaN.
 constexpr float kFar = 0x1p-76f;  // 2^20 squares of values below 2^128
 
 __device__ __forceinline__ float rstd_of_far(float sq, float inv, float eps) {
@@ -235,7 +236,8 @@ __host__ __device__ inline int64_t sums_pitch(int64_t cols) { return (cols + 3) 
 // worked on. A block's groups take equally many turns, so that its barriers meet.
 // Measured, 16384 x 4096 bf16 with dresidual: 91-92 us (5.8-5.9 TB/s) and 4.6 for
 // the join; two blocks a CU instead of one are no faster there and 10 % slower
-// at 8192 x 1600 fp16 (28 us with the join, 29 with dresidual). All of it goes past the caches (115 -> 107 us).
+// at 8192 x 1600 fp16 (28 us with the join, 29 with dresidual). All of it goes past
+// the caches (115 -> 107 us).
 template <int DT, int V, int W, int G, bool RES>
 __global__ void __launch_bounds__(64 * W * G, 2) norm_grad_kernel(const NormGradArgs N) {
   constexpr int kVals = Vec<DT>::kVals, kElem = Vec<DT>::kElem;
