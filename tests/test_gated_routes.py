@@ -24,6 +24,9 @@ MEASURED = {
     (2550, 1024, 2856): (119.4, 82.3), (647, 3408, 608): (38.3, 28.8), (474, 4216, 504): (34.0, 24.5),
     (2960, 344, 19952): (391.4, 350.9), (1576, 776, 17120): (376.0, 312.6), (2787, 1088, 13440): (481.3, 453.2),
     (3159, 384, 19256): (385.0, 410.0), (1031, 2712, 520): (37.5, 49.6), (1648, 312, 3392): (56.2, 74.7),
+    (451, 776, 976): (40.6, 31.8), (712, 2704, 280): (35.0, 28.3), (666, 2816, 256): (41.5, 26.8),
+    (558, 2224, 336): (41.7, 31.9), (1203, 1648, 576): (47.7, 37.4), (1777, 336, 344): (33.8, 52.7),
+    (1043, 264, 704): (31.5, 39.4), (1870, 1000, 976): (58.1, 72.2), (903, 880, 256): (29.6, 36.8),
     (2118, 1088, 1032): (55.1, 57.3), (256, 4096, 4096): (65.7, 65.3), (8033, 328, 17136): (930.4, 820.4),
 }
 

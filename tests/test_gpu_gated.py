@@ -416,7 +416,8 @@ def test_small_values_of_far_gates(act, lo, hi, ws):
 
 
 @pytest.mark.parametrize("dt", DTS)
-@pytest.mark.parametrize("size", [(700, 1280, 5120), (153, 1344, 7920), (1410, 1584, 1504), (4096, 1024, 1024), (2001, 400, 264)],
+@pytest.mark.parametrize("size", [(700, 1280, 5120), (153, 1344, 7920), (1410, 1584, 1504), (451, 776, 976), (4096, 1024, 1024),
+                                  (2001, 400, 264)],
                          ids=str)
 def test_backward_at_sizes_on_both_sides_of_the_shared_launch(size, dt, ws):
     """Shared launches with dx in splits and with large, middle and small tiles for dw alone; and sizes beside them that

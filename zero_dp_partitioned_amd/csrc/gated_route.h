@@ -92,20 +92,9 @@ inline PairRoute pair_route(int64_t m, int64_t d, int64_t f, int64_t room) {
     r.together = true;
     return r;
   }
-  // Where dw alone shares its contraction among blocks, a large tile, which does all
-  // of it, is the whole launch's time: of 21 sizes 18 took up to 3.6 times as long
-  // together (4096 x 1024 x 1024 66, 115; 8192 x 512 x 512 49, 176), three small ones 3
-  // to 19 % less (712 x 2704 x 280 35, 28).
-  if (w.splits > 1) return r;
-  // Between the two, by when the last block ends: a stage of a middle tile takes 0.55
-  // us, one of a large tile 1.45 and its ends 6, a launch 2. An XCD's 32 CUs take its
-  // share of dx's blocks first, then of dw's. Of sizes with a round of dw's tiles at
-  // most, 59 that end within three quarters of the time apart took from 4 % more to
-  // 36 % less together (2079 x 1000 x 3776 133, 91; 1500 x 1608 x 1000 52, 46; 2118 x 1088 x
-  // 1032 55, 57), 74 others from 6 % less to 34 % more (1500 x 1600 x 640 38, 43; 2048 x
-  // 768 x 3000 87, 99; 3953 x 672 x 2624, where an XCD gets one block too many, 111,
-  // 149). With more than a round 13 up to 0.84 took as long to 26 % less (2960 x 344 x
-  // 19952 391, 351), three above it 6 % more.
+  // Else by when the last block ends: a stage of a middle tile takes 0.55 us, one of a
+  // large tile 1.45 and its ends 6. An XCD's 32 CUs take its share of dx's blocks
+  // first, then of dw's; a large tile does all of its contraction.
   const double tx = 0.55 * chunks / r.splits, tw = 1.45 * tiles_over(m, kChunk) + 6;
   const int64_t cus = kCus / kXcds, busy = tiles_over(r.dx_blocks, kXcds);
   double idle_from = 0, dx_from = tx, end = tx;
@@ -116,7 +105,21 @@ inline PairRoute pair_route(int64_t m, int64_t d, int64_t f, int64_t room) {
     from += tw;
     end = end > from ? end : from;
   }
-  r.together = end <= (r.tiles > kCus ? 0.85 : 0.75) * (tx + tw * tiles_over(r.tiles, kCus) + 2);
+  // Apart, dw takes as long as its large tiles and a launch, 2. Of sizes with a round of
+  // them at most, 59 that end within three quarters of that time took from 4 % more to
+  // 36 % less together (2079 x 1000 x 3776 133, 91; 1500 x 1608 x 1000 52, 46; 2118 x 1088 x
+  // 1032 55, 57), 74 others from 6 % less to 34 % more (1500 x 1600 x 640 38, 43; 2048 x
+  // 768 x 3000 87, 99; 3953 x 672 x 2624, where an XCD gets one block too many, 111,
+  // 149). With more than a round 13 up to 0.84 took as long to 26 % less (2960 x 344 x
+  // 19952 391, 351), three above it 6 % more.
+  // A dw that shares its contraction among blocks takes every CU, and 22 for its
+  // launches, its ends and the join: of 23 sizes within nine tenths of that time 21
+  // took 2 to 35 % less together (451 x 776 x 976 41, 32; 712 x 2704 x 280 35, 28), two 4
+  // and 5 % more; of 61 others 58 took up to 3.6 times as long (4096 x 1024 x 1024 66,
+  // 115; 8192 x 512 x 512 49, 176), three up to 11 % less.
+  const bool shares = w.splits > 1;
+  const double alone = shares ? 4.0 / 3 * r.tiles * (tw - 6) / kCus + 22 : tw * tiles_over(r.tiles, kCus) + 2;
+  r.together = end <= (shares ? 0.9 : r.tiles > kCus ? 0.85 : 0.75) * (tx + alone);
   return r;
 }
 
