@@ -136,9 +136,11 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) norm_kernel(const NormA
     float rstd = 1.0f / sqrtf(sq * N.inv + N.eps);
     if (__builtin_expect(!__builtin_isfinite(sq), 0)) {
       sq = 0.f;
+      int again = lane;
+      asm volatile("" : "+v"(again));  // the masks of `skip` are made anew, or they would be held up to here
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const Slot<DT, W> slot(j, w, lane, N.cols);
+        const Slot<DT, W> slot(j, w, again, N.cols);
 #pragma unroll
         for (int e = 0; e < kVals; ++e) {
           const float d = e >= slot.skip ? v[j][e] * kFar : 0.f;
