@@ -97,7 +97,7 @@ struct Slot {
 
 // W waves a row, V 16-byte slots a lane; a block of one wave a row has four
 // rows. At least Vec<DT>::kVals columns. Measured: 16384 x 4096 bf16 50 us (5.4
-// TB/s), 8192 x 1600 fp16 12.7 (4.1), one row of 4096 3.0 in a graph. The output
+// TB/s), 8192 x 1600 fp16 12.5 (4.2), one row of 4096 3.0 in a graph. The output
 // goes past the caches, the input does not: with the hint on both the first took 1 %
 // more and the second, which the caches hold, 4 %.
 template <int DT, int V, int W>
